@@ -228,6 +228,38 @@ BF_API bf_status_t bifocal_prefill_chunk_paged(const void* q, const void* k, con
                                                int32_t page_size, const int32_t* block_table, int32_t max_pages,
                                                void* out, float* lse, void* stream);
 
+/* Causal prefill of a packed batch: sequences of different lengths laid one after another, each with
+ * its own positions from 0 and its own G = max(1, ceil(L_b / w_pretrained)). Rows see only rows of
+ * their own sequence: sequence b's results are those of bifocal_prefill on its rows alone.
+ *   q    [total_rows, hq,  D] raw, dtype;  k, v [total_rows, hkv, D] raw, dtype
+ *   cu_seqlens [batch + 1] int32 (device): sequence b is rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1; a
+ *          sequence may be empty; rows before cu_seqlens[0] and from cu_seqlens[batch] on belong to none:
+ *          they are not read, and nothing is written for them
+ *   max_len: an upper bound of every L_b (host)
+ *   out  [total_rows, hq, D] bf16, written;  lse [hq, total_rows] fp32, written (may be NULL)
+ *   kcache, vcache [cache_rows, hkv, D] bf16 (both or neither): every key under the ORIGINAL RoPE and its
+ *          value, at its packed row (block_table NULL; cache_rows >= total_rows), or at row
+ *          block_table[b * max_pages + j / page_size] * page_size + j % page_size for key j of sequence b
+ *          (cache_rows = pages * page_size, max_pages * page_size >= max_len, any page_size >= 1)
+ *   kpos [hkv, cache_rows] int32 (may be NULL; needs the caches): the position of each key written, per
+ *          kv head, as bifocal_cache_evict and bifocal_decode_kept read it
+ *   workspace / ws_bytes: >= bifocal_prefill_packed_workspace_size(dtype, batch, total_rows, p), 256-byte
+ *          aligned: the rotated operand forms (fp16), a bf16 copy of fp32 values and the list of tiles.
+ * Boundaries that are not in order, exceed total_rows or give a length above max_len are reported as
+ * BF_ERR_INDEX by bifocal_last_device_error, and nothing is written. A block-table entry outside the
+ * pool is reported likewise and its rows are not written; the attention does not read the cache.
+ * Flags: BF_FLAG_WINDOW as for bifocal_prefill; BF_FLAG_FORCE_BIFOCAL and BF_FLAG_FUSED_ROPE change nothing.
+ * Errors: as bifocal_prefill; BF_ERR_INVALID also for NULL cu_seqlens, total_rows or max_len < 1 and bad
+ * cache arguments; BF_ERR_UNSUPPORTED for BF_FLAG_MMA_SYNC. */
+BF_API size_t bifocal_prefill_packed_workspace_size(int32_t dtype, int32_t batch, int32_t total_rows,
+                                                    const bf_params_t* p);
+BF_API bf_status_t bifocal_prefill_packed(const void* q, const void* k, const void* v, int32_t dtype,
+                                          int32_t total_rows, int32_t batch, const int32_t* cu_seqlens,
+                                          int32_t max_len, const bf_params_t* p, void* out, float* lse, void* kcache,
+                                          void* vcache, int32_t* kpos, int64_t cache_rows, int32_t page_size,
+                                          const int32_t* block_table, int32_t max_pages, void* workspace,
+                                          size_t ws_bytes, void* stream);
+
 /* Bytes of device workspace bifocal_decode / rope_causal_decode need for a cache of up to
  * L_max rows: the split-KV partial results (fp32). Host only. 0 on invalid arguments. */
 BF_API size_t bifocal_decode_workspace_size(int32_t L_max, const bf_params_t* p);

@@ -17,6 +17,7 @@ __all__ = [
     "BifocalError", "FREQ_INTERP", "POS_ALIAS", "FLAG_FORCE_BIFOCAL", "FLAG_MMA_SYNC", "FLAG_WINDOW", "FLAG_FUSED_ROPE", "Params", "lib", "lib_path",
     "bifocal_factor", "bifocal_prefill", "bifocal_prefill_rope", "bifocal_prefill_attention", "rope_causal_prefill", "bifocal_prefill_chunk_paged", "bifocal_decode", "bifocal_decode_noalloc", "rope_causal_decode",
     "prefill_workspace_size", "decode_workspace_size", "last_device_error", "build_info", "test_set_fault",
+    "bifocal_prefill_packed", "prefill_packed_workspace_size",
     "STATUS_TIMEOUT", "STATUS_RANGE", "STATUS_INDEX", "FAULT_NONE", "FAULT_PREFILL_SKIP_FILL", "FAULT_DECODE_SKIP_STAGE",
 ]
 
@@ -95,6 +96,11 @@ def _lib() -> ctypes.CDLL:
         L.bifocal_prefill_chunk_paged.argtypes = [vp, vp, vp, i32, vp, vp, pp, vp, vp, i32, i32, vp, i32, vp, vp,
                                                   vp]
         L.bifocal_prefill_chunk_paged.restype = i32
+        L.bifocal_prefill_packed_workspace_size.argtypes = [i32, i32, i32, pp]
+        L.bifocal_prefill_packed_workspace_size.restype = sz
+        L.bifocal_prefill_packed.argtypes = [vp, vp, vp, i32, i32, i32, vp, i32, pp, vp, vp, vp, vp, vp, i64, i32, vp, i32,
+                                             vp, sz, vp]
+        L.bifocal_prefill_packed.restype = i32
         L.bifocal_decode_noalloc.argtypes = [vp, vp, vp, vp, vp, i32, i32, pp, vp, vp, vp]
         L.bifocal_decode_noalloc.restype = i32
         L.bifocal_status_string.argtypes, L.bifocal_status_string.restype = [i32], ctypes.c_char_p
@@ -360,6 +366,96 @@ def rope_causal_decode(q, k_new, v_new, kcache, vcache, L: int, *, theta: float,
                        want_lse: bool = True, out=None, workspace=None, stream=None):
     p = make_params(q.shape[0], k_new.shape[0], q.shape[1], 0, 1, theta, FREQ_INTERP, scale, 0)
     return _decode("rope_causal_decode", q, k_new, v_new, kcache, vcache, L, p, want_lse, out, workspace, stream)
+
+
+# ---------------------------------------------------------------------------------------------
+# Packed prompts and cache eviction
+# ---------------------------------------------------------------------------------------------
+def _operands(where: str, **tensors):
+    """Checks the tensors of a call (None = not given): CUDA, one device, contiguous. Returns the device."""
+    device = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda or not t.is_contiguous():
+            raise BifocalError(1, f"{where}: {name} must be a contiguous CUDA tensor")
+        if device is not None and t.device != device:
+            raise BifocalError(1, f"{where}: {name} is on {t.device}, other tensors on {device}")
+        device = t.device
+    return device
+
+
+def _expect(where: str, name: str, t, shape, *dtypes):
+    """Checks a tensor's shape (-1 = any) and type."""
+    if t is None:
+        return
+    if t.dim() != len(shape) or any(w != -1 and n != w for n, w in zip(t.shape, shape)):
+        raise BifocalError(1, f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if dtypes and t.dtype not in dtypes:
+        raise BifocalError(1, f"{where}: {name} has type {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+
+
+class _On:
+    """The device of a call's tensors made current, and the call's stream on it (default: that device's
+    current stream): what the call allocates belongs to that stream."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.guard = torch.cuda.device(device)
+        self.stream = torch.cuda.current_stream(device) if stream is None else stream
+        self.on = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        self.guard.__enter__()
+        self.on.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        self.on.__exit__(*exc)
+        return self.guard.__exit__(*exc)
+
+
+def prefill_packed_workspace_size(dtype: int, batch: int, total_rows: int, params: Params) -> int:
+    return int(_lib().bifocal_prefill_packed_workspace_size(dtype, int(batch), int(total_rows), ctypes.byref(params)))
+
+
+def bifocal_prefill_packed(q, k, v, cu_seqlens, max_len: int, *, w0: int, w_pretrained: int, theta: float,
+                           mode: str = FREQ_INTERP, scale: Optional[float] = None, flags: int = 0,
+                           want_lse: bool = True, kcache=None, vcache=None, kpos=None, page_size: int = 0,
+                           block_table=None, out=None, workspace=None, stream=None):
+    """Causal prefill of packed sequences. q [T, Hq, D], k / v [T, Hkv, D] raw (bf16 or fp32); cu_seqlens [B + 1]
+    int32 on the device; max_len bounds the lengths. kcache / vcache [rows, Hkv, D] bf16 (and kpos [Hkv, rows]
+    int32) receive the keys under the original RoPE, the values and positions: at the packed rows, or through
+    block_table [B, max_pages] int32 and page_size. Returns (out [T, Hq, D] bf16, lse [Hq, T] fp32 or None); rows
+    of no sequence are left as they were (in a new `out` or lse: unspecified)."""
+    import torch
+    fn = "bifocal_prefill_packed"
+    dev = _operands(fn, q=q, k=k, v=v, cu_seqlens=cu_seqlens, kcache=kcache, vcache=vcache, kpos=kpos,
+                    block_table=block_table, out=out, workspace=workspace)
+    _expect(fn, "q", q, (-1, -1, -1))
+    T, hq, D = q.shape
+    dt = _dtype_code(q)
+    _expect(fn, "k", k, (T, -1, D), q.dtype)
+    hkv = k.shape[1]
+    _expect(fn, "v", v, (T, hkv, D), q.dtype)
+    _expect(fn, "cu_seqlens", cu_seqlens, (-1,), torch.int32)
+    B = cu_seqlens.numel() - 1
+    _expect(fn, "out", out, (T, hq, D), torch.bfloat16)
+    rows = kcache.shape[0] if kcache is not None else 0
+    _expect(fn, "kcache", kcache, (rows, hkv, D), torch.bfloat16)
+    _expect(fn, "vcache", vcache, (rows, hkv, D), torch.bfloat16)
+    _expect(fn, "kpos", kpos, (hkv, rows), torch.int32)
+    _expect(fn, "block_table", block_table, (B, -1), torch.int32)
+    p = make_params(hq, hkv, D, w0, w_pretrained, theta, mode, scale, flags)
+    with _On(dev, stream) as st:
+        out = torch.empty(T, hq, D, dtype=torch.bfloat16, device=dev) if out is None else out
+        lse = torch.empty(hq, T, dtype=torch.float32, device=dev) if want_lse else None
+        ws = _workspace(prefill_packed_workspace_size(dt, B, T, p), dev) if workspace is None else workspace
+        _check(_lib().bifocal_prefill_packed(
+            _ptr(q), _ptr(k), _ptr(v), dt, T, B, _ptr(cu_seqlens), int(max_len), ctypes.byref(p), _ptr(out), _ptr(lse),
+            _ptr(kcache), _ptr(vcache), _ptr(kpos), rows, int(page_size), _ptr(block_table),
+            0 if block_table is None else block_table.shape[1], _ptr(ws), ws.numel() * ws.element_size(), st), fn)
+    return out, lse
 
 
 def device_status_word() -> int:

@@ -13,6 +13,7 @@
 #include "../../include/bifocal.h"
 #include "common.cuh"
 #include "decode.cuh"
+#include "packed.cuh"
 #include "prefill_mma.cuh"
 #include "prefill_tc.cuh"
 #include "prefill_tc2.cuh"
@@ -1227,3 +1228,5 @@ const char* bifocal_build_info(void) {
 }
 
 }  // extern "C"
+
+#include "packed_host.cuh"

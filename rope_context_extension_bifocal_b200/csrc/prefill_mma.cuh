@@ -11,6 +11,7 @@
 // forming the subtracted terms.
 #pragma once
 #include "common.cuh"
+#include "packed.cuh"
 
 namespace bf {
 
@@ -26,6 +27,7 @@ struct AttnArgs {
   float* lse;                // [b, hq, L] or null
   int L, hq, hkv, w0;
   float scale_log2;  // softmax scale * log2(e)
+  PackedTiles packed;  // PACKED only: L is then unused
 };
 
 namespace mma_cfg {
@@ -52,7 +54,8 @@ __device__ __forceinline__ void load_tile_async(uint32_t sbase, const T* g, long
   }
 }
 
-template <int D, bool BIFOCAL>
+// PACKED: a batch of packed sequences; blockIdx.x is the rank in the tile list.
+template <int D, bool BIFOCAL, bool PACKED = false>
 __global__ void __launch_bounds__(256, 1) attn_mma_kernel(const __grid_constant__ AttnArgs a) {
   using namespace mma_cfg;
   constexpr int KC = D / 16;  // k-chunks of the QK^T contraction
@@ -66,24 +69,36 @@ __global__ void __launch_bounds__(256, 1) attn_mma_kernel(const __grid_constant_
   const uint32_t sK = sQ + NV * QTILE;                   // [2 stages][NV][BN][D]
   const uint32_t sV = sK + 2 * NV * KTILE;               // [2 stages][BN][D]
 
-  const int n_qt = (a.L + BM - 1) / BM;
-  const int qt = n_qt - 1 - blockIdx.x;  // heaviest tiles first
-  const int h = blockIdx.y, b = blockIdx.z;
+  // the sequence's length L; its first row row0; rows a head (pitch)
+  int i0, L = a.L, row0 = 0, pitch = a.L, w0 = a.w0;
+  const int h = blockIdx.y, b = PACKED ? 0 : blockIdx.z;
+  if (PACKED) {
+    const int rank = blockIdx.x;
+    if (rank >= a.packed.head->n_tiles) return;
+    const int2 tile = a.packed.tiles[rank];
+    i0 = tile.y * BM;
+    row0 = a.packed.cu[tile.x];
+    L = a.packed.cu[tile.x + 1] - row0;
+    pitch = a.packed.total_rows;
+    if (BIFOCAL && !has_long_pairs(L, factor_of(L, a.packed.w_pretrained), w0)) w0 = kAllLocal;
+  } else {
+    const int n_qt = (a.L + BM - 1) / BM;
+    const int qt = n_qt - 1 - blockIdx.x;  // heaviest tiles first
+    i0 = qt * BM;
+  }
   const int kvh = h / (a.hq / a.hkv);
-  const int i0 = qt * BM;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int w0 = a.w0;
 
-  const long long qoff = (static_cast<long long>(b) * a.hq + h) * a.L * D + static_cast<long long>(i0) * D;
-  const long long koff = (static_cast<long long>(b) * a.hkv + kvh) * a.L * D;
-  const __nv_bfloat16* Vg = a.V + b * a.v_batch_stride + kvh * D;
+  const long long qoff = ((static_cast<long long>(b) * a.hq + h) * pitch + row0 + i0) * D;
+  const long long koff = ((static_cast<long long>(b) * a.hkv + kvh) * pitch + row0) * D;
+  const __nv_bfloat16* Vg = a.V + b * a.v_batch_stride + row0 * a.v_row_stride + kvh * D;
 
-  const int qvalid = min(BM, a.L - i0);
+  const int qvalid = min(BM, L - i0);
   load_tile_async<D, BM>(sQ, a.Qo + qoff, D, qvalid);
   if (BIFOCAL) load_tile_async<D, BM>(sQ + QTILE, a.Ql + qoff, D, qvalid);
   cp_async_commit();
 
-  const int kv_end = min(i0 + BM, a.L);
+  const int kv_end = min(i0 + BM, L);
   const int n_kt = (kv_end + BN - 1) / BN;
 
   auto tile_needs = [&](int j0, bool& need_o, bool& need_l) {
@@ -98,7 +113,7 @@ __global__ void __launch_bounds__(256, 1) attn_mma_kernel(const __grid_constant_
   };
   auto issue_kv = [&](int t) {
     const int j0 = t * BN, st = t & 1;
-    const int valid = min(BN, a.L - j0);
+    const int valid = min(BN, L - j0);
     bool no, nl;
     tile_needs(j0, no, nl);
     const uint32_t kb = sK + st * NV * KTILE;
@@ -243,16 +258,16 @@ __global__ void __launch_bounds__(256, 1) attn_mma_kernel(const __grid_constant_
     lsum += __shfl_xor_sync(0xffffffffu, lsum, 1);
     lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
     const int i = iw + g8 + r * 8;
-    if (i < a.L) {
+    if (i < L) {
       const float inv = 1.f / lsum;
-      __nv_bfloat16* orow = a.out + ((static_cast<long long>(b) * a.L + i) * a.hq + h) * D;
+      __nv_bfloat16* orow = a.out + ((static_cast<long long>(b) * a.L + row0 + i) * a.hq + h) * D;
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) {
         const uint32_t pk = pack_bf16x2(o[dt][2 * r] * inv, o[dt][2 * r + 1] * inv);
         *reinterpret_cast<uint32_t*>(orow + dt * 8 + 2 * t4) = pk;
       }
       if (a.lse && t4 == 0)
-        a.lse[(static_cast<long long>(b) * a.hq + h) * a.L + i] = (m_r[r] + __log2f(lsum)) * 0.69314718055994530942f;
+        a.lse[(static_cast<long long>(b) * a.hq + h) * pitch + row0 + i] = (m_r[r] + __log2f(lsum)) * 0.69314718055994530942f;
     }
   }
 }

@@ -24,6 +24,8 @@
 // merge without forming the subtracted terms.
 #pragma once
 #include "common.cuh"
+#include "packed.cuh"
+#include "rope_loads.cuh"
 
 namespace bf {
 namespace tc {
@@ -113,6 +115,7 @@ struct TcArgs {
   float* lse;          // [b, hq, L] or null
   int L, hq, hkv, batch, w0;
   float scale_log2;
+  PackedTiles packed;  // PACKED only: L and batch are then unused
 };
 
 // Visits of key tile t for the query tile starting at i0: kinds (and how many, 1 or 2).
@@ -141,7 +144,8 @@ __device__ __forceinline__ int tile_visits(int i0, int t, int w0, int (&kinds)[2
   return 1;
 }
 
-template <bool BIFOCAL>
+// PACKED: a batch of packed sequences (as in attn_tc2_kernel).
+template <bool BIFOCAL, bool PACKED = false>
 __global__ void __launch_bounds__(tc::NTHREADS, 1) attn_tc_kernel(const __grid_constant__ TcArgs a) {
   using namespace tc;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -151,14 +155,29 @@ __global__ void __launch_bounds__(tc::NTHREADS, 1) attn_tc_kernel(const __grid_c
   __shared__ float red[2][2][BM];  // [visit parity][column half][row]: row maxima, then row sums
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n_qt = (a.L + BM - 1) / BM;
-  const int per_tile = a.hq * a.batch;
-  const int qt = n_qt - 1 - static_cast<int>(blockIdx.x) / per_tile;  // heaviest first
-  const int rem = static_cast<int>(blockIdx.x) % per_tile;
-  const int h = rem % a.hq, b = rem / a.hq;
+  // rows: the sequence's length L; row0 its first row in q, k, v, out and lse; pitch: rows a head
+  int h, b, i0, L = a.L, row0 = 0, pitch = a.L, w0 = a.w0;
+  if (PACKED) {
+    const int rank = static_cast<int>(blockIdx.x) / a.hq;
+    if (rank >= a.packed.head->n_tiles) return;
+    const int2 tile = a.packed.tiles[rank];
+    h = static_cast<int>(blockIdx.x) % a.hq;
+    b = 0;
+    i0 = tile.y * BM;
+    row0 = a.packed.cu[tile.x];
+    L = a.packed.cu[tile.x + 1] - row0;
+    pitch = a.packed.total_rows;
+    if (BIFOCAL && !has_long_pairs(L, factor_of(L, a.packed.w_pretrained), w0)) w0 = kAllLocal;
+  } else {
+    const int n_qt = (a.L + BM - 1) / BM;
+    const int per_tile = a.hq * a.batch;
+    const int qt = n_qt - 1 - static_cast<int>(blockIdx.x) / per_tile;  // heaviest first
+    const int rem = static_cast<int>(blockIdx.x) % per_tile;
+    h = rem % a.hq, b = rem / a.hq;
+    i0 = qt * BM;
+  }
   const int kvh = h / (a.hq / a.hkv);
-  const int i0 = qt * BM;
-  const int n_kt = (min(i0 + BM, a.L) + BN - 1) / BN;
+  const int n_kt = (min(i0 + BM, L) + BN - 1) / BN;
   const uint32_t slots = smem_u32(smem);
 
   if (threadIdx.x == 0) {
@@ -197,7 +216,7 @@ __global__ void __launch_bounds__(tc::NTHREADS, 1) attn_tc_kernel(const __grid_c
       bool ok = true;
       for (int t = 0; t < n_kt && ok; ++t) {
         int kinds[2];
-        const int nv = tile_visits<BIFOCAL>(i0, t, a.w0, kinds);
+        const int nv = tile_visits<BIFOCAL>(i0, t, w0, kinds);
         for (int vi = 0; vi < nv && ok; ++vi) {
           const bool lng = kinds[vi] == LONG_FULL || kinds[vi] == LONG_ONLY;
           for (int x = 0; x < 2 && ok; ++x, ++n) {
@@ -210,11 +229,11 @@ __global__ void __launch_bounds__(tc::NTHREADS, 1) attn_tc_kernel(const __grid_c
             uint8_t* dst = smem + slot * SLOT_BYTES;
             if (x == 0) {
               const CUtensorMap* m = lng ? &a.kl_map : &a.ko_map;
-              tma_load_3d(dst, m, &full[slot], 0, t * BN, krow);
-              tma_load_3d(dst + HALF_BYTES, m, &full[slot], 64, t * BN, krow);
+              tma_load_3d(dst, m, &full[slot], 0, row0 + t * BN, krow);
+              tma_load_3d(dst + HALF_BYTES, m, &full[slot], 64, row0 + t * BN, krow);
             } else {
-              tma_load_4d(dst, &a.v_map, &full[slot], 0, kvh, t * BN, b);
-              tma_load_4d(dst + HALF_BYTES, &a.v_map, &full[slot], 64, kvh, t * BN, b);
+              tma_load_4d(dst, &a.v_map, &full[slot], 0, kvh, row0 + t * BN, b);
+              tma_load_4d(dst + HALF_BYTES, &a.v_map, &full[slot], 64, kvh, row0 + t * BN, b);
             }
           }
         }
@@ -232,7 +251,7 @@ __global__ void __launch_bounds__(tc::NTHREADS, 1) attn_tc_kernel(const __grid_c
       int prev_vslot = -1;
       for (int t = 0; t < n_kt && ok; ++t) {
         int kinds[2];
-        const int nv = tile_visits<BIFOCAL>(i0, t, a.w0, kinds);
+        const int nv = tile_visits<BIFOCAL>(i0, t, w0, kinds);
         for (int vi = 0; vi < nv && ok; ++vi, ++v) {
           const bool lng = kinds[vi] == LONG_FULL || kinds[vi] == LONG_ONLY;
           const int ks = (2 * v) % NSLOT, vs = (2 * v + 1) % NSLOT;
@@ -305,7 +324,7 @@ __global__ void __launch_bounds__(tc::NTHREADS, 1) attn_tc_kernel(const __grid_c
     // Q (both RoPE forms) into TMEM: lane = row, 64 columns of fp16 pairs each; each half
     // of the row's threads writes 32 columns of each form
     {
-      const long long qrow = ((static_cast<long long>(b) * a.hq + h) * a.L + i) * D;
+      const long long qrow = ((static_cast<long long>(b) * a.hq + h) * pitch + row0 + i) * D;
       for (int f = 0; f < (BIFOCAL ? 2 : 1); ++f) {
         const __half* src = (f == 0 ? a.Qo : a.Ql) + qrow;
         const int c0 = 32 * half;
@@ -313,7 +332,7 @@ __global__ void __launch_bounds__(tc::NTHREADS, 1) attn_tc_kernel(const __grid_c
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (i < a.L) x = reinterpret_cast<const uint4*>(src)[c0 / 4 + u];
+          if (i < L) x = reinterpret_cast<const uint4*>(src)[c0 / 4 + u];
           reg[4 * u + 0] = x.x;
           reg[4 * u + 1] = x.y;
           reg[4 * u + 2] = x.z;
@@ -334,7 +353,7 @@ __global__ void __launch_bounds__(tc::NTHREADS, 1) attn_tc_kernel(const __grid_c
     bool ok = true;
     for (int t = 0; t < n_kt; ++t) {
       int kinds[2];
-      const int nv = tile_visits<BIFOCAL>(i0, t, a.w0, kinds);
+      const int nv = tile_visits<BIFOCAL>(i0, t, w0, kinds);
       const int j0 = t * BN;
       for (int vi = 0; vi < nv; ++vi, ++v) {
         const int kind = kinds[vi];
@@ -353,8 +372,8 @@ __global__ void __launch_bounds__(tc::NTHREADS, 1) attn_tc_kernel(const __grid_c
           const bool masked = kind != LONG_FULL && (kind != ORIG_FULL || j0 + BN - 1 > i0);
           if (masked) {
             const int d0 = i - j0 - 64 * half;  // i - j for this thread's first column
-            const int lo = (kind == LONG_ONLY) ? a.w0 : 0;            // keep lo <= i - j
-            const int hi = (kind == ORIG_LOCAL) ? a.w0 : 0x7fffffff;  //      and i - j < hi
+            const int lo = (kind == LONG_ONLY) ? w0 : 0;            // keep lo <= i - j
+            const int hi = (kind == ORIG_LOCAL) ? w0 : 0x7fffffff;  //      and i - j < hi
 #pragma unroll
             for (int c = 0; c < 64; ++c) {
               const int d = d0 - c;
@@ -419,6 +438,17 @@ __global__ void __launch_bounds__(tc::NTHREADS, 1) attn_tc_kernel(const __grid_c
               }
             }
           }
+          if (PACKED && ok && j0 + BN > L) {
+            // value rows past the sequence's end are zeroed before P.V reads them (0 * NaN is NaN);
+            // the wait is for this visit's own fill, as in attn_tc2_kernel
+            ok = __all_sync(0xffffffffu, mbar_wait_abortable(&full[(2 * v + 1) % NSLOT], ((2 * v + 1) / NSLOT) & 1, 33,
+                                                             &s_abort));
+            if (ok) {
+              const int st = threadIdx.x - 64;  // the 256 softmax threads
+              zero_tile_rows(slots + (2 * v + 1) % NSLOT * SLOT_BYTES, L - j0, st & 7, st >> 3, 32);
+              fence_proxy_async_smem();
+            }
+          }
           wait_st();
           fence_before();
           __syncwarp();
@@ -434,13 +464,13 @@ __global__ void __launch_bounds__(tc::NTHREADS, 1) attn_tc_kernel(const __grid_c
     if (fin) {
       fence_after();
       const float inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
-      __nv_bfloat16* orow = a.out + ((static_cast<long long>(b) * a.L + i) * a.hq + h) * D + 64 * half;
+      __nv_bfloat16* orow = a.out + ((static_cast<long long>(b) * a.L + row0 + i) * a.hq + h) * D + 64 * half;
 #pragma unroll 1
       for (int c = 0; c < 64; c += 32) {
         float ov[32];
         tmem_ld32(lane_addr + COL_O + 64 * half + c, ov);
         wait_ld();
-        if (i < a.L) {
+        if (i < L) {
 #pragma unroll
           for (int u = 0; u < 32; u += 8) {
             uint4 w;
@@ -452,8 +482,8 @@ __global__ void __launch_bounds__(tc::NTHREADS, 1) attn_tc_kernel(const __grid_c
           }
         }
       }
-      if (half == 0 && a.lse && i < a.L)
-        a.lse[(static_cast<long long>(b) * a.hq + h) * a.L + i] = (m_ref + __log2f(l_sum)) * 0.69314718055994530942f;
+      if (half == 0 && a.lse && i < L)
+        a.lse[(static_cast<long long>(b) * a.hq + h) * pitch + row0 + i] = (m_ref + __log2f(l_sum)) * 0.69314718055994530942f;
     }
   }
 

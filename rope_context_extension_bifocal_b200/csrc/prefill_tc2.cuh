@@ -26,6 +26,7 @@
 // one Q form in shared memory at a time.
 #pragma once
 #include "common.cuh"
+#include "packed.cuh"
 #include "prefill_tc.cuh"
 #include "rope_loads.cuh"
 
@@ -142,6 +143,7 @@ struct Tc2Args {
   int tile_start[tc2::kMaxSeqs + 1];
   int seq_id[tc2::kMaxSeqs], seq_P0[tc2::kMaxSeqs], seq_C[tc2::kMaxSeqs], seq_G[tc2::kMaxSeqs],
       seq_qrow[tc2::kMaxSeqs];
+  PackedTiles packed;  // PACKED only: L, q_off, Lq and batch are then unused
 };
 
 // FUSED = false: Q and K tiles come by TMA from the RoPE pass's fp16 forms; K and V share a
@@ -149,7 +151,10 @@ struct Tc2Args {
 // FUSED = true: TMA brings the raw bf16 tiles; warps 10 and 11 rotate Q and K in place into
 // fp16 operands (rope_loads.cuh); K has its own ring of three slots, V of two. No rotated
 // copy of q or k exists in HBM.
-template <int KIND, bool FUSED>
+// PACKED = true (unfused): a batch of packed sequences. Q, K and V rows are packed rows, a CTA's
+// query tile comes from the tile list, and value rows past the sequence's end (the next
+// sequence's, or no one's) are zeroed in shared memory before the last P.V reads them.
+template <int KIND, bool FUSED, bool PACKED = false>
 __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __grid_constant__ Tc2Args a) {
   using namespace tc2;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -181,6 +186,20 @@ __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __gri
     G = a.seq_G[sq];
     qrow0 = a.seq_qrow[sq];
     qt = (Lq + BM - 1) / BM - 1 - (tile - a.tile_start[sq]);  // heaviest first within the sequence
+  } else if (PACKED) {
+    // kv-head major as below; within a head the tiles of all sequences, heaviest first
+    const int ppk = pairs / a.hkv;
+    const int idx = static_cast<int>(blockIdx.x);
+    const int rank = idx / ppk % a.packed.max_tiles;
+    if (rank >= a.packed.head->n_tiles) return;
+    const int2 tile = a.packed.tiles[rank];
+    hp = idx / (ppk * a.packed.max_tiles) * ppk + idx % ppk;
+    b = 0;
+    qrow0 = a.packed.cu[tile.x];
+    Lq = a.packed.cu[tile.x + 1] - qrow0;
+    q_off = 0;
+    qt = tile.y;
+    G = factor_of(Lq, a.packed.w_pretrained);
   } else {
     // kv-head major: the CTAs resident at one time share one kv head's K and V tiles (the key
     // forms of one head fit in L2 at 128K, those of all eight do not: with the query tiles of
@@ -205,7 +224,8 @@ __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __gri
   const int kvh = h0 / (a.hq / a.hkv);
   const int i0 = q_off + qt * BM;  // absolute position of the tile's first query row
   const int n_kt = (min(i0 + BM, L) + BN - 1) / BN;
-  const Schedule sch = make_schedule<KIND>(i0, n_kt, a.w0);
+  const int w0 = (PACKED && KIND == KIND_BIFOCAL && !has_long_pairs(L, G, a.w0)) ? kAllLocal : a.w0;
+  const Schedule sch = make_schedule<KIND>(i0, n_kt, w0);
   const int nv = sch.total();
   const bool has_long = sch.n_long() > 0;
   const bool has_orig = sch.n_bl + sch.n_of > 0;
@@ -304,8 +324,9 @@ __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __gri
               tma_load_4d(dst + HALF_BYTES, &a.qo_map, bar, 64, h0 + x, row, bb);
             } else {
               const CUtensorMap* m = lng ? &a.ql_map : &a.qo_map;
-              tma_load_3d(dst, m, bar, 0, qt * BM, b * a.hq + h0 + x);
-              tma_load_3d(dst + HALF_BYTES, m, bar, 64, qt * BM, b * a.hq + h0 + x);
+              const int row = (PACKED ? qrow0 : 0) + qt * BM;
+              tma_load_3d(dst, m, bar, 0, row, b * a.hq + h0 + x);
+              tma_load_3d(dst + HALF_BYTES, m, bar, 64, row, b * a.hq + h0 + x);
             }
           }
         };
@@ -362,12 +383,14 @@ __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __gri
           mbar_arrive_expect_tx(bar, SLOT_BYTES);
           if (x == 1 || FUSED) {
             const CUtensorMap* m = x == 0 ? &a.ko_map : &a.v_map;
-            tma_load_4d(dst, m, bar, 0, kvh, t * BN, b);
-            tma_load_4d(dst + HALF_BYTES, m, bar, 64, kvh, t * BN, b);
+            const int row = (PACKED ? qrow0 : 0) + t * BN;
+            tma_load_4d(dst, m, bar, 0, kvh, row, b);
+            tma_load_4d(dst + HALF_BYTES, m, bar, 64, kvh, row, b);
           } else {
             const CUtensorMap* m = lng ? &a.kl_map : &a.ko_map;
-            tma_load_3d(dst, m, bar, 0, t * BN, krow);
-            tma_load_3d(dst + HALF_BYTES, m, bar, 64, t * BN, krow);
+            const int row = (PACKED ? qrow0 : 0) + t * BN;
+            tma_load_3d(dst, m, bar, 0, row, krow);
+            tma_load_3d(dst + HALF_BYTES, m, bar, 64, row, krow);
           }
           return true;
         };
@@ -602,8 +625,8 @@ __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __gri
       }
       fence_after();
       const bool masked = kind != LONG_FULL && (kind != ORIG_FULL || j0 + BN - 1 > i0);
-      const int lo = (kind == LONG_ONLY) ? a.w0 : 0;            // keep lo <= i - j
-      const int hi = (kind == ORIG_LOCAL) ? a.w0 : 0x7fffffff;  //      and i - j < hi
+      const int lo = (kind == LONG_ONLY) ? w0 : 0;            // keep lo <= i - j
+      const int hi = (kind == ORIG_LOCAL) ? w0 : 0x7fffffff;  //      and i - j < hi
       float alpha = 1.f, rs = 0.f;
       bool grow = false;
       uint32_t pk[64];  // P of the whole row, bf16 pairs (keys 2u, 2u + 1 in pk[u])
@@ -791,6 +814,19 @@ __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __gri
           }
         }
       }
+      if (PACKED && x == 0 && j0 + BN > L) {
+        // Value rows past the sequence's end: P is 0 there, but 0 * NaN is NaN. These four warps
+        // zero them once the tile has landed; neither tile's P.V of this visit is issued before
+        // all four have arrived on p_lo[0] (the visit is masked, so it was not sent yet). The wait
+        // is for this visit's own fill: the slot's previous one was read by a P.V issued before
+        // this visit's S, and its next one waits for this visit's P.V.
+        if (!__all_sync(0xffffffffu, mbar_wait_abortable(v_full(v), v_full_ph(v), 35, &s_abort))) {
+          ok = false;
+          break;
+        }
+        zero_tile_rows(vslots + v_slot(v) * SLOT_BYTES, L - j0, threadIdx.x & 7, threadIdx.x >> 3, 16);
+        fence_proxy_async_smem();
+      }
       wait_st();
       fence_before();
       __syncwarp();
@@ -828,7 +864,7 @@ __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __gri
         report_status(kDevRange, 45);
       if (a.lse && rel < Lq) {
         // dense: [b, hq, Lq]; a paged batch: [hq, total_rows] over the packed rows
-        const long long li = paged ? static_cast<long long>(h) * a.total_rows + qrow0 + rel
+        const long long li = paged || PACKED ? static_cast<long long>(h) * (PACKED ? a.packed.total_rows : a.total_rows) + qrow0 + rel
                                    : (static_cast<long long>(b) * a.hq + h) * a.Lq + rel;
         a.lse[li] = (m_ref + __log2f(l_sum)) * 0.69314718055994530942f;
       }

@@ -199,11 +199,10 @@ __device__ __forceinline__ void rope_key_tile(uint32_t slot, const RopeSrc& s, i
 
 // Zeroes the rows r_lo .. 127 of a V tile (both halves): the keys past a sequence's end in a
 // paged pool, whose P is 0 but whose values may be anything (0 * NaN would be NaN).
-__device__ __forceinline__ void zero_tile_rows(uint32_t slot, int r_lo, int cch, int r0) {
+__device__ __forceinline__ void zero_tile_rows(uint32_t slot, int r_lo, int cch, int r0, int step = 8) {
   const uint4 z = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 1
-  for (int m = 0; m < 16; ++m) {
-    const int r = r0 + 8 * m;
+  for (int r = r0; r < 128; r += step) {
     if (r >= r_lo) {
       st_shared16(slot + slot_off(r, cch), z);
       st_shared16(slot + 16384 + slot_off(r, cch), z);

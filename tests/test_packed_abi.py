@@ -1,0 +1,61 @@
+"""Argument validation of the packed-prompt and cache-eviction entry points: every refusal comes
+before any CUDA call, so none of this needs a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+import rope_context_extension_bifocal_b200 as bfl
+from tests.test_abi import FAKE, lib, params  # noqa: F401  (fixture)
+
+INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 5
+
+
+def test_prefill_packed_validation(lib):
+    f = lib.bifocal_prefill_packed
+
+    def call(p=None, q=FAKE, k=FAKE, cu=FAKE, T=100, B=3, max_len=60, dtype=0, out=FAKE, lse=None, kc=None, vc=None,
+             kpos=None, rows=0, page=0, table=None, max_pages=0, ws=FAKE, wsb=0):
+        return f(q, k, FAKE, dtype, T, B, cu, max_len, ctypes.byref(p or params()), out, lse, kc, vc, kpos, rows, page,
+                 table, max_pages, ws, wsb, None)
+
+    assert call() == WORKSPACE  # valid up to the (empty) workspace
+    assert call(ws=None) == WORKSPACE
+    assert call(ws=FAKE + 16, wsb=1 << 40) == WORKSPACE
+    for bad in (dict(q=None), dict(k=FAKE + 4), dict(cu=None), dict(cu=FAKE + 2), dict(out=None), dict(out=FAKE + 2),
+                dict(lse=FAKE + 1), dict(T=0), dict(B=0), dict(max_len=0), dict(p=params(w0=-1)),
+                dict(p=params(w_pretrained=0)), dict(p=params(hq=30)), dict(p=params(theta=1.0)),
+                dict(p=params(flags=bfl.FLAG_WINDOW, w0=0)),
+                dict(kc=FAKE), dict(kpos=FAKE), dict(kc=FAKE, vc=FAKE), dict(kc=FAKE, vc=FAKE, rows=99),
+                dict(kc=FAKE, vc=FAKE + 2, rows=100), dict(kc=FAKE, vc=FAKE, kpos=FAKE + 1, rows=100),
+                dict(kc=FAKE, vc=FAKE, rows=96, table=FAKE, page=0, max_pages=8),
+                dict(kc=FAKE, vc=FAKE, rows=100, table=FAKE, page=16, max_pages=8),   # not whole pages
+                dict(kc=FAKE, vc=FAKE, rows=96, table=FAKE, page=16, max_pages=3),    # 48 < max_len
+                dict(kc=FAKE, vc=FAKE, rows=96, table=FAKE + 2, page=16, max_pages=8),
+                dict(kc=FAKE, vc=FAKE, rows=1 << 31, table=None)):
+        assert call(**bad) == INVALID, bad
+    for bad in (dict(dtype=5), dict(p=params(head_dim=96)), dict(p=params(flags=bfl.FLAG_MMA_SYNC)),
+                dict(p=params(flags=bfl.FLAG_WINDOW, w0=8, hq=24)),
+                dict(p=params(flags=bfl.FLAG_WINDOW, w0=8, head_dim=64))):
+        assert call(**bad) == UNSUPPORTED, bad
+    for good in (dict(kc=FAKE, vc=FAKE, rows=100), dict(kc=FAKE, vc=FAKE, rows=96, table=FAKE, page=48, max_pages=2)):
+        assert call(**good) == WORKSPACE, good
+
+
+def test_prefill_packed_workspace_size(lib):
+    T, B = 1000, 4
+    s = bfl.prefill_packed_workspace_size(bfl.DTYPE_BF16, B, T, params())
+    forms = 2 * (T * 32 * 128 * 2) + 2 * (T * 8 * 128 * 2)
+    assert forms < s <= forms + 4096
+    assert bfl.prefill_packed_workspace_size(bfl.DTYPE_FP32, B, T, params()) == s + T * 8 * 128 * 2
+    assert bfl.prefill_packed_workspace_size(bfl.DTYPE_BF16, 0, T, params()) == 0
+    assert bfl.prefill_packed_workspace_size(bfl.DTYPE_BF16, B, 0, params()) == 0
+    assert bfl.prefill_packed_workspace_size(9, B, T, params()) == 0
+
+
+def test_binding_refuses_cpu_and_strided_tensors(lib):
+    q = torch.zeros(4, 2, 128, dtype=torch.bfloat16)
+    cu = torch.tensor([0, 4], dtype=torch.int32)
+    with pytest.raises(bfl.BifocalError) as e:
+        bfl.bifocal_prefill_packed(q, q, q, cu, 4, w0=1, w_pretrained=8, theta=1e6)
+    assert e.value.status == INVALID
