@@ -312,6 +312,66 @@ BF_API bf_status_t bifocal_decode_paged(const void* q, const void* k_new, const 
                                         int32_t max_len, int32_t batch, const bf_params_t* p, void* out,
                                         float* lse, void* workspace, size_t ws_bytes, void* stream);
 
+/* Cuts the caches of a batch of sequences to `budget` slots each, by the attention weight their keys
+ * have received (kweight, accumulated by bifocal_key_weights and bifocal_decode_kept), every kv head by its
+ * own. A slot is a place of a sequence's cache: slot s of sequence b is pool row
+ * block_table[b * max_pages + s / page_size] * page_size + s % page_size; kpos tells, per kv head, the
+ * position the key in it came from.
+ *   kcache, vcache [cache_rows, hkv, head_dim] bf16;  kpos [hkv, cache_rows] int32;  kweight [hkv, cache_rows] fp32
+ *   seq_lens [batch] int32 (device): n_b, the slots in use, 0 <= n_b <= max_len (host)
+ *   positions [batch] int32 (device): the position of sequence b's newest token
+ *   budget >= 1; recent, sink >= 0 with recent + sink <= budget
+ * Of a sequence and kv head min(n_b, budget) slots are kept, chosen in this order: slots whose position
+ * is below sink or above positions[b] - recent, then the others by descending weight (NaN as -inf), equal
+ * ones by ascending slot. new_lens [batch] int32 (device; may be seq_lens) receives min(n_b, budget).
+ *   dst_block_table NULL: in place. Kept slots below min(n_b, budget) stay; the i-th kept slot from there
+ *          on moves (key, value, position, weight) to the i-th slot below that was not kept.
+ *   dst_block_table [batch, dst_max_pages] (device): the i-th kept slot is copied to slot i under this
+ *          table (pages of the same pool, dst_max_pages * page_size >= min(max_len, budget)); the source rows
+ *          stay as they are. Its pages must be none of those the call reads.
+ * No page may appear twice among the rows written. Rows that receive no kept slot are left as they were.
+ *   workspace / ws_bytes: >= bifocal_cache_evict_workspace_size(batch, hkv, max_len, budget), 256-byte aligned.
+ * A length outside [0, max_len] is reported as BF_ERR_INDEX by bifocal_last_device_error and that sequence left
+ * as it is (new_lens[b] = seq_lens[b]); a table entry outside the pool likewise, its slots rank last and
+ * are not moved.
+ * Errors: BF_ERR_INVALID for NULL or misaligned pointers, sizes < 1, recent + sink > budget, rows that are
+ * not whole pages or tables too short; BF_ERR_UNSUPPORTED for head_dim not 64/128, batch or hkv > 65535. */
+BF_API size_t bifocal_cache_evict_workspace_size(int32_t batch, int32_t hkv, int32_t max_len, int32_t budget);
+BF_API bf_status_t bifocal_cache_evict(void* kcache, void* vcache, int32_t* kpos, float* kweight, int64_t cache_rows,
+                                       int32_t page_size, const int32_t* block_table, int32_t max_pages,
+                                       const int32_t* dst_block_table, int32_t dst_max_pages, const int32_t* seq_lens,
+                                       const int32_t* positions, int32_t* new_lens, int32_t batch, int32_t hkv,
+                                       int32_t head_dim, int32_t max_len, int32_t budget, int32_t recent,
+                                       int32_t sink, void* workspace, size_t ws_bytes, void* stream);
+
+/* One decode step for a batch of sequences over kept slots: as bifocal_decode_paged, but the key in a slot
+ * has the position kpos gives it (per kv head, in any order), and the new token's position is given
+ * apart from the number of slots.
+ *   q [batch, hq, D], k_new, v_new [batch, hkv, D] bf16 raw
+ *   kcache, vcache [cache_rows, hkv, D] bf16, keys under the ORIGINAL RoPE; kpos [hkv, cache_rows] int32
+ *   kweight [hkv, cache_rows] fp32 or NULL: to every slot in use the step adds the attention weight its key
+ *          received, summed over the query heads of its kv head
+ *   seq_lens [batch] int32 (device): n_b, slots in use with the new token's, 1 <= n_b <= max_len (host); slot
+ *          n_b - 1 is written: the key under the original RoPE, the value, the position, and the step's weight
+ *   positions [batch] int32 (device): the new token's position p_b, >= 0. G = max(1, ceil((p_b + 1) / w_pretrained));
+ *          a key of position j is local if p_b - j < w0
+ *   block_table [batch, max_pages] int32 (device), page_size >= 1, max_pages * page_size >= max_len
+ *   out [batch, hq, D] bf16;  lse [batch, hq] fp32 (may be NULL)
+ *   workspace / ws_bytes: >= bifocal_decode_kept_workspace_size(batch, max_len, kweight != NULL, p), 256-byte aligned.
+ * Scores, softmax and weights are formed in fp32 (no fp16 operands). Slots past a sequence's length are
+ * not read. A length or position out of range is reported as BF_ERR_INDEX by bifocal_last_device_error, appends
+ * nothing and gives NaN as that sequence's output; a table entry outside the pool is reported, its keys
+ * and values read as zeros and nothing of its rows is written.
+ * Flags: BF_FLAG_WINDOW keeps only keys with p_b - j < w0, under the original RoPE (w0 >= 1); the others
+ * change nothing. Errors: as bifocal_decode_paged. */
+BF_API size_t bifocal_decode_kept_workspace_size(int32_t batch, int32_t max_len, int32_t accumulate,
+                                                 const bf_params_t* p);
+BF_API bf_status_t bifocal_decode_kept(const void* q, const void* k_new, const void* v_new, void* kcache, void* vcache,
+                                       int32_t* kpos, float* kweight, int64_t cache_rows, int32_t page_size,
+                                       const int32_t* block_table, int32_t max_pages, const int32_t* seq_lens,
+                                       const int32_t* positions, int32_t max_len, int32_t batch, const bf_params_t* p,
+                                       void* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
+
 /* bifocal_decode without a caller workspace, for callers that cannot allocate device memory
  * themselves: for example a plug-in hosted by a runtime that owns and pre-plans all device
  * memory, or a latency-critical loop that may not call cudaMalloc (which synchronises the

@@ -17,7 +17,8 @@ __all__ = [
     "BifocalError", "FREQ_INTERP", "POS_ALIAS", "FLAG_FORCE_BIFOCAL", "FLAG_MMA_SYNC", "FLAG_WINDOW", "FLAG_FUSED_ROPE", "Params", "lib", "lib_path",
     "bifocal_factor", "bifocal_prefill", "bifocal_prefill_rope", "bifocal_prefill_attention", "rope_causal_prefill", "bifocal_prefill_chunk_paged", "bifocal_decode", "bifocal_decode_noalloc", "rope_causal_decode",
     "prefill_workspace_size", "decode_workspace_size", "last_device_error", "build_info", "test_set_fault",
-    "bifocal_prefill_packed", "prefill_packed_workspace_size",
+    "bifocal_prefill_packed", "prefill_packed_workspace_size", "bifocal_cache_evict", "cache_evict_workspace_size",
+    "bifocal_decode_kept", "decode_kept_workspace_size",
     "STATUS_TIMEOUT", "STATUS_RANGE", "STATUS_INDEX", "FAULT_NONE", "FAULT_PREFILL_SKIP_FILL", "FAULT_DECODE_SKIP_STAGE",
 ]
 
@@ -101,6 +102,16 @@ def _lib() -> ctypes.CDLL:
         L.bifocal_prefill_packed.argtypes = [vp, vp, vp, i32, i32, i32, vp, i32, pp, vp, vp, vp, vp, vp, i64, i32, vp, i32,
                                              vp, sz, vp]
         L.bifocal_prefill_packed.restype = i32
+        L.bifocal_decode_kept_workspace_size.argtypes = [i32, i32, i32, pp]
+        L.bifocal_decode_kept_workspace_size.restype = sz
+        L.bifocal_decode_kept.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i32, vp, i32, vp, vp, i32, i32, pp, vp, vp, vp,
+                                          sz, vp]
+        L.bifocal_decode_kept.restype = i32
+        L.bifocal_cache_evict_workspace_size.argtypes = [i32, i32, i32, i32]
+        L.bifocal_cache_evict_workspace_size.restype = sz
+        L.bifocal_cache_evict.argtypes = [vp, vp, vp, vp, i64, i32, vp, i32, vp, i32, vp, vp, vp, i32, i32, i32, i32, i32,
+                                          i32, i32, vp, sz, vp]
+        L.bifocal_cache_evict.restype = i32
         L.bifocal_decode_noalloc.argtypes = [vp, vp, vp, vp, vp, i32, i32, pp, vp, vp, vp]
         L.bifocal_decode_noalloc.restype = i32
         L.bifocal_status_string.argtypes, L.bifocal_status_string.restype = [i32], ctypes.c_char_p
@@ -455,6 +466,86 @@ def bifocal_prefill_packed(q, k, v, cu_seqlens, max_len: int, *, w0: int, w_pret
             _ptr(q), _ptr(k), _ptr(v), dt, T, B, _ptr(cu_seqlens), int(max_len), ctypes.byref(p), _ptr(out), _ptr(lse),
             _ptr(kcache), _ptr(vcache), _ptr(kpos), rows, int(page_size), _ptr(block_table),
             0 if block_table is None else block_table.shape[1], _ptr(ws), ws.numel() * ws.element_size(), st), fn)
+    return out, lse
+
+
+def cache_evict_workspace_size(batch: int, hkv: int, max_len: int, budget: int) -> int:
+    return int(_lib().bifocal_cache_evict_workspace_size(int(batch), int(hkv), int(max_len), int(budget)))
+
+
+def bifocal_cache_evict(kcache, vcache, kpos, kweight, page_size: int, block_table, seq_lens, positions, max_len: int,
+                        budget: int, *, recent: int, sink: int = 0, dst_block_table=None, new_lens=None, workspace=None,
+                        stream=None):
+    """Cuts every sequence's cache to `budget` slots by the weight its keys received. kcache / vcache [rows, Hkv, D]
+    bf16, kpos [Hkv, rows] int32, kweight [Hkv, rows] fp32; block_table [B, max_pages], seq_lens [B] (slots in use)
+    and positions [B] (the newest token's) int32 on the device; max_len bounds seq_lens. Positions below `sink` and the
+    newest `recent` ones are kept first, then the largest weights. In place, or to the pages of dst_block_table in slot
+    order. Returns new_lens [B] int32 = min(seq_lens, budget) (may be given; may be seq_lens)."""
+    import torch
+    fn = "bifocal_cache_evict"
+    dev = _operands(fn, kcache=kcache, vcache=vcache, kpos=kpos, kweight=kweight, block_table=block_table,
+                    seq_lens=seq_lens, positions=positions, dst_block_table=dst_block_table, new_lens=new_lens,
+                    workspace=workspace)
+    _expect(fn, "kcache", kcache, (-1, -1, -1), torch.bfloat16)
+    rows, hkv, D = kcache.shape
+    _expect(fn, "vcache", vcache, (rows, hkv, D), torch.bfloat16)
+    _expect(fn, "kpos", kpos, (hkv, rows), torch.int32)
+    _expect(fn, "kweight", kweight, (hkv, rows), torch.float32)
+    _expect(fn, "seq_lens", seq_lens, (-1,), torch.int32)
+    B = seq_lens.numel()
+    _expect(fn, "positions", positions, (B,), torch.int32)
+    _expect(fn, "block_table", block_table, (B, -1), torch.int32)
+    _expect(fn, "dst_block_table", dst_block_table, (B, -1), torch.int32)
+    _expect(fn, "new_lens", new_lens, (B,), torch.int32)
+    with _On(dev, stream) as st:
+        new_lens = torch.empty_like(seq_lens) if new_lens is None else new_lens
+        ws = _workspace(cache_evict_workspace_size(B, hkv, max_len, budget), dev) if workspace is None else workspace
+        _check(_lib().bifocal_cache_evict(
+            _ptr(kcache), _ptr(vcache), _ptr(kpos), _ptr(kweight), rows, int(page_size), _ptr(block_table),
+            block_table.shape[1], _ptr(dst_block_table), 0 if dst_block_table is None else dst_block_table.shape[1],
+            _ptr(seq_lens), _ptr(positions), _ptr(new_lens), B, hkv, D, int(max_len), int(budget), int(recent), int(sink),
+            _ptr(ws), ws.numel() * ws.element_size(), st), fn)
+    return new_lens
+
+
+def decode_kept_workspace_size(batch: int, max_len: int, accumulate: bool, params: Params) -> int:
+    return int(_lib().bifocal_decode_kept_workspace_size(int(batch), int(max_len), int(accumulate), ctypes.byref(params)))
+
+
+def bifocal_decode_kept(q, k_new, v_new, kcache, vcache, kpos, kweight, page_size: int, block_table, seq_lens, positions,
+                        max_len: int, *, w0: int, w_pretrained: int, theta: float, mode: str = FREQ_INTERP,
+                        scale: Optional[float] = None, flags: int = 0, want_lse: bool = True, out=None, workspace=None,
+                        stream=None):
+    """One decode step over kept slots. q [B, Hq, D], k_new / v_new [B, Hkv, D] bf16; kcache / vcache [rows, Hkv, D]
+    bf16, kpos [Hkv, rows] int32 (each key's position), kweight [Hkv, rows] fp32 (each key's weight, added to) or None;
+    block_table [B, max_pages], seq_lens [B] (slots with the new token's) and positions [B] (the new token's) int32 on
+    the device; max_len bounds seq_lens. Returns (out [B, Hq, D], lse [B, Hq] or None)."""
+    import torch
+    fn = "bifocal_decode_kept"
+    dev = _operands(fn, q=q, k_new=k_new, v_new=v_new, kcache=kcache, vcache=vcache, kpos=kpos, kweight=kweight,
+                    block_table=block_table, seq_lens=seq_lens, positions=positions, out=out, workspace=workspace)
+    _expect(fn, "q", q, (-1, -1, -1), torch.bfloat16)
+    B, hq, D = q.shape
+    _expect(fn, "kcache", kcache, (-1, -1, D), torch.bfloat16)
+    rows, hkv, _ = kcache.shape
+    _expect(fn, "vcache", vcache, (rows, hkv, D), torch.bfloat16)
+    _expect(fn, "k_new", k_new, (B, hkv, D), torch.bfloat16)
+    _expect(fn, "v_new", v_new, (B, hkv, D), torch.bfloat16)
+    _expect(fn, "kpos", kpos, (hkv, rows), torch.int32)
+    _expect(fn, "kweight", kweight, (hkv, rows), torch.float32)
+    _expect(fn, "seq_lens", seq_lens, (B,), torch.int32)
+    _expect(fn, "positions", positions, (B,), torch.int32)
+    _expect(fn, "block_table", block_table, (B, -1), torch.int32)
+    _expect(fn, "out", out, (B, hq, D), torch.bfloat16)
+    p = make_params(hq, hkv, D, w0, w_pretrained, theta, mode, scale, flags)
+    with _On(dev, stream) as st:
+        out = torch.empty(B, hq, D, dtype=torch.bfloat16, device=dev) if out is None else out
+        lse = torch.empty(B, hq, dtype=torch.float32, device=dev) if want_lse else None
+        ws = _workspace(decode_kept_workspace_size(B, max_len, kweight is not None, p), dev) if workspace is None else workspace
+        _check(_lib().bifocal_decode_kept(
+            _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(kcache), _ptr(vcache), _ptr(kpos), _ptr(kweight), rows,
+            int(page_size), _ptr(block_table), block_table.shape[1], _ptr(seq_lens), _ptr(positions), int(max_len), B,
+            ctypes.byref(p), _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), st), fn)
     return out, lse
 
 

@@ -13,6 +13,8 @@
 #include "../../include/bifocal.h"
 #include "common.cuh"
 #include "decode.cuh"
+#include "decode_kept.cuh"
+#include "evict.cuh"
 #include "packed.cuh"
 #include "prefill_mma.cuh"
 #include "prefill_tc.cuh"

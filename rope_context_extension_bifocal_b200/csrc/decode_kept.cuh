@@ -1,0 +1,459 @@
+// Decode over kept slots: a paged cache whose slots no longer are positions.
+//
+// After an eviction slot s of a kv head holds the key of some position kpos[head, row], another one
+// in every head. A step appends the new token at slot n - 1 and attends to all n slots, each key
+// under the branch its own position asks for; with kweight it then adds to every slot the attention
+// weight its key received, summed over the head's group.
+//
+// One rotation for both branches. The cache holds R_o(j) k. With q' = R_l(i) q, the long-range score
+// is <q', C(j) R_o(j) k> with C(p) = R_l(p) R_o(p)^-1, and the local one
+//   <R_o(i) q, R_o(j) k> = <R_l(i) R_o(i)^-1 R_o(i) q, C(i) R_o(j) k> = <q', C(i) R_o(j) k>,
+// so every key is turned by C(its position, or the query's when it is local): one form of the query,
+// no branch per key, and keys of both kinds may lie in any order. C(p) turns pair k by m(p) c_k,
+// with m = p, c_k = w_k (1/G - 1) under frequency interpolation and m = p - floor(p / G), c_k = -w_k
+// under position aliasing. c_k is held as a fraction of a turn, 32 bits of it as an integer and the
+// rest as a float: the integer product m c_k wraps at whole turns by itself, so the reduced angle
+// costs an integer multiplication and an FMA, exact to 2^-23 turns at any position.
+//
+// What bounds it: 4 D bytes of K and V a slot and kv head from HBM, and, next to that, instructions
+// (about 50 a slot and kv head and warp for four query heads at D = 128: half of them the sines and
+// cosines, which no table can share since every head has positions of its own). QK^T and PV run on
+// packed fp32 FMAs: with at most 8 query rows they cost less than the conversions and the split
+// operands that the tensor cores would need to keep scores, and so weights, exact to fp32.
+//
+// Work split: a CTA takes a range of slots of one (sequence, kv head), a warp every fourth chunk of
+// it; D / 8 lanes share a key (4 pairs each). A second kernel merges the ranges and adds the weights.
+// Padded to 1, 2, 4 or 8 query heads a kv head (GP).
+#pragma once
+#include "common.cuh"
+#include "packed.cuh"
+
+namespace bf {
+
+namespace kept {
+constexpr int WARPS = 4;
+constexpr int NK = 4;       // keys a lane group holds at a time
+constexpr int MAX_G = 8;    // query heads per kv head (max)
+}  // namespace kept
+
+struct KeptArgs {
+  const __nv_bfloat16* q;      // [B, hq, D] raw
+  const __nv_bfloat16* k_new;  // [B, hkv, D] raw
+  const __nv_bfloat16* v_new;
+  __nv_bfloat16* kcache;       // [rows, hkv, D]
+  __nv_bfloat16* vcache;
+  int* kpos;                   // [hkv, rows]
+  float* kweight;              // [hkv, rows] or null
+  CacheRows rows;
+  const int* seq_lens;         // [B] slots with the new token's
+  const int* positions;        // [B] position of the new token
+  int hq, hkv, w0, w_pretrained, mode, window, max_len;
+  int split_len, n_split;
+  float scale_log2;
+  float* part_o;               // [B, hq, n_split, D] unnormalised
+  float* part_ml;              // [B, hq, n_split, 2]: max (log2 domain), sum
+  float* scores;               // [B, hq, pitch] log2-domain scores (with kweight)
+  int pitch;
+  __nv_bfloat16* out;          // [B, hq, D]
+  float* lse;                  // [B, hq] or null
+  double omega[64];
+};
+
+// What a sequence's CTAs agree on.
+struct KeptSeq {
+  int n, now, G;
+  bool ok, rot;
+};
+
+__device__ __forceinline__ KeptSeq kept_seq(const KeptArgs& a, int b) {
+  KeptSeq s;
+  s.n = a.seq_lens[b];
+  s.now = a.positions[b];
+  s.ok = s.n >= 1 && s.n <= a.max_len && s.now >= 0 && s.now < 0x7fffffff;
+  s.G = s.ok ? factor_of(s.now + 1, a.w_pretrained) : 1;
+  s.rot = !a.window && s.G > 1 && a.w0 <= s.now;  // some position 0 .. now is in the long-range branch
+  return s;
+}
+
+__device__ __forceinline__ int far_multiple(int p, int G, int mode) { return mode == 0 ? p : p - p / G; }
+
+template <int D, int GP>
+__global__ void __launch_bounds__(kept::WARPS * 32) decode_kept_kernel(const __grid_constant__ KeptArgs a) {
+  using namespace kept;
+  constexpr int P = D / 2;
+  constexpr int LPK = D / 8;        // lanes a key
+  constexpr int KPW = 32 / LPK;     // keys side by side in a warp
+  constexpr int CH = NK * KPW;      // keys of a warp's chunk
+  constexpr int NV = NK * GP;       // scores a lane group reduces
+  constexpr int OWN = NV > LPK ? NV / LPK : 1;  // of which a lane keeps this many
+  __shared__ __align__(16) float sp[WARPS][KPW][NV];
+  __shared__ float sm[WARPS][GP], sl[WARPS][GP];
+  __shared__ __align__(16) float so[WARPS][GP][D];
+
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ll = lane % LPK, kg = lane / LPK;
+  const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
+  const int g = a.hq / a.hkv;
+  pdl_wait();
+  const KeptSeq seq = kept_seq(a, b);
+  if (!seq.ok) {
+    if (threadIdx.x == 0) report_status(kDevIndex, 70);
+    return;
+  }
+  const int s_beg = split * a.split_len, s_end = min(seq.n, s_beg + a.split_len);
+  if (s_beg >= s_end) return;
+
+  // the query heads' rows under R_l(now) (R_o when nothing is long-range), in the log2 domain, and
+  // the turn fractions of the correction: this lane's pairs 4 ll .. 4 ll + 3
+  uint64_t q2[GP][4];  // packed pairs: x of pairs (0,1), (2,3); y of pairs (0,1), (2,3)
+  uint32_t whi[4];
+  float wlo[4];
+  {
+    float c[4], s[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const double w = a.omega[4 * ll + e];
+      const double ang = !seq.rot ? static_cast<double>(seq.now) * w
+                         : a.mode == 0 ? static_cast<double>(seq.now) * (w / seq.G)
+                                       : static_cast<double>(seq.now / seq.G) * w;
+      angle_cos_sin(ang, c[e], s[e]);
+      double t = (a.mode == 0 ? w / seq.G - w : -w) * 0.15915494309189533576888376337251;  // turns a unit of m
+      t = (t - floor(t)) * 4294967296.0;
+      const double hi = fmin(floor(t), 4294967295.0);
+      whi[e] = static_cast<uint32_t>(hi);
+      wlo[e] = static_cast<float>((t - hi) * 2.3283064365386962890625e-10);
+    }
+#pragma unroll
+    for (int h = 0; h < GP; ++h) {
+      float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+      if (h < g) {
+        const __nv_bfloat16* qr = a.q + (static_cast<long long>(b) * a.hq + kvh * g + h) * D + 4 * ll;
+        const uint2 u = *reinterpret_cast<const uint2*>(qr), w = *reinterpret_cast<const uint2*>(qr + P);
+        const float2 u0 = unpack_bf16x2(u.x), u1 = unpack_bf16x2(u.y), w0 = unpack_bf16x2(w.x), w1 = unpack_bf16x2(w.y);
+        const float xr[4] = {u0.x, u0.y, u1.x, u1.y}, yr[4] = {w0.x, w0.y, w1.x, w1.y};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = (xr[e] * c[e] - yr[e] * s[e]) * a.scale_log2;
+          y[e] = (yr[e] * c[e] + xr[e] * s[e]) * a.scale_log2;
+        }
+      }
+      q2[h][0] = f2_pack(x[0], x[1]);
+      q2[h][1] = f2_pack(x[2], x[3]);
+      q2[h][2] = f2_pack(y[0], y[1]);
+      q2[h][3] = f2_pack(y[2], y[3]);
+    }
+  }
+  const int m_now = far_multiple(seq.now, seq.G, a.mode);
+
+  // Row, position and validity of the chunk's key i = lane % CH (key n of lane group kg is i = n * KPW + kg)
+  auto lookup = [&](int base, int& row, int& pos) {
+    const int slot = base + lane % CH;
+    row = -1;
+    pos = seq.now;
+    if (slot < s_end) {
+      const long long r = cache_row(a.rows, b, slot, 0);
+      if (r < 0) {
+        report_status(kDevIndex, 71);
+      } else {
+        row = static_cast<int>(r);
+        if (slot != seq.n - 1) pos = a.kpos[static_cast<long long>(kvh) * a.rows.rows + row];
+      }
+    }
+  };
+  auto load = [&](int row, uint2 (&kx)[NK], uint2 (&ky)[NK], uint4 (&v)[NK]) {
+#pragma unroll
+    for (int n = 0; n < NK; ++n) {
+      const int r = __shfl_sync(0xffffffffu, row, n * KPW + kg);
+      kx[n] = ky[n] = make_uint2(0u, 0u);
+      v[n] = make_uint4(0u, 0u, 0u, 0u);
+      if (r >= 0) {
+        const long long at = (static_cast<long long>(r) * a.hkv + kvh) * D;
+        kx[n] = *reinterpret_cast<const uint2*>(a.kcache + at + 4 * ll);
+        ky[n] = *reinterpret_cast<const uint2*>(a.kcache + at + P + 4 * ll);
+        v[n] = *reinterpret_cast<const uint4*>(a.vcache + at + 8 * ll);
+      }
+    }
+  };
+
+  uint64_t o2[GP][4];
+#pragma unroll
+  for (int h = 0; h < GP; ++h)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o2[h][e] = f2_pack(0.f, 0.f);
+  // Score idx = n * GP + h of a lane group ends, after the reduction, with lane idx * LPK / NV of it:
+  // a lane keeps OWN scores from own0 on (or shares one with the LPK / NV - 1 lanes after it).
+  const int own0 = ll * NV / LPK;
+  const bool first_copy = NV >= LPK || ll % (LPK / NV > 0 ? LPK / NV : 1) == 0;
+  float m_own[OWN], l_own[OWN];  // running maximum (of the whole warp) and own sum, per own score's head
+#pragma unroll
+  for (int u = 0; u < OWN; ++u) m_own[u] = -INFINITY, l_own[u] = 0.f;
+  // lane bits that select the head of a score; the others select the key or a copy
+  auto head_bit = [](int mask) { return mask < LPK && mask * NV / LPK >= 1 && mask * NV / LPK < GP; };
+
+  uint2 kx[NK], ky[NK], nkx[NK], nky[NK];
+  uint4 v[NK], nv[NK];
+  int row, pos, nrow, npos;
+  int base = s_beg + warp * CH;
+  if (base < s_end) {
+    lookup(base, nrow, npos);
+    load(nrow, nkx, nky, nv);
+  }
+  for (; base < s_end; base += WARPS * CH) {
+    row = nrow;
+    pos = npos;
+#pragma unroll
+    for (int n = 0; n < NK; ++n) kx[n] = nkx[n], ky[n] = nky[n], v[n] = nv[n];
+    if (base + WARPS * CH < s_end) {
+      lookup(base + WARPS * CH, nrow, npos);
+      load(nrow, nkx, nky, nv);
+    }
+    // the new token's key and value: rotated, rounded to the cache's bf16, appended and used from there
+    if (base + CH >= seq.n && seq.n > base) {
+#pragma unroll
+      for (int n = 0; n < NK; ++n) {
+        const int r = __shfl_sync(0xffffffffu, row, n * KPW + kg);
+        if (base + n * KPW + kg == seq.n - 1) {
+          const long long src = (static_cast<long long>(b) * a.hkv + kvh) * D;
+          const uint2 u = *reinterpret_cast<const uint2*>(a.k_new + src + 4 * ll);
+          const uint2 w = *reinterpret_cast<const uint2*>(a.k_new + src + P + 4 * ll);
+          const float2 u0 = unpack_bf16x2(u.x), u1 = unpack_bf16x2(u.y), w0 = unpack_bf16x2(w.x), w1 = unpack_bf16x2(w.y);
+          const float xr[4] = {u0.x, u0.y, u1.x, u1.y}, yr[4] = {w0.x, w0.y, w1.x, w1.y};
+          float x[4], y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float c, s;
+            angle_cos_sin(static_cast<double>(seq.now) * a.omega[4 * ll + e], c, s);
+            x[e] = xr[e] * c - yr[e] * s;
+            y[e] = yr[e] * c + xr[e] * s;
+          }
+          kx[n] = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+          ky[n] = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+          v[n] = *reinterpret_cast<const uint4*>(a.v_new + src + 8 * ll);
+          if (r >= 0) {
+            const long long at = (static_cast<long long>(r) * a.hkv + kvh) * D;
+            *reinterpret_cast<uint2*>(a.kcache + at + 4 * ll) = kx[n];
+            *reinterpret_cast<uint2*>(a.kcache + at + P + 4 * ll) = ky[n];
+            *reinterpret_cast<uint4*>(a.vcache + at + 8 * ll) = v[n];
+            if (ll == 0) a.kpos[static_cast<long long>(kvh) * a.rows.rows + r] = seq.now;
+          }
+        }
+      }
+    }
+    // scores: this lane's share of each (key, head), then the sum over the key's lanes
+    const bool is_local = seq.now - pos < a.w0;
+    const int mult = is_local ? m_now : far_multiple(pos, seq.G, a.mode);
+    float val[NV];
+#pragma unroll
+    for (int n = 0; n < NK; ++n) {
+      uint64_t x0 = bf16x2_to_f2(kx[n].x), x1 = bf16x2_to_f2(kx[n].y);
+      uint64_t y0 = bf16x2_to_f2(ky[n].x), y1 = bf16x2_to_f2(ky[n].y);
+      if (seq.rot) {
+        const int m = __shfl_sync(0xffffffffu, mult, n * KPW + kg);
+        const float mf = static_cast<float>(m);
+        float c[4], s[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // turns in [-1/2, 1/2): the top bits of the wrapped product as the mantissa of a float in [1, 2)
+          const uint32_t ph = static_cast<uint32_t>(m) * whi[e] + 0x80000100u;
+          const float t = __uint_as_float((ph >> 9) | 0x3f800000u) - 1.5f;
+          __sincosf(fmaf(mf, wlo[e], t) * 6.283185307179586f, &s[e], &c[e]);
+        }
+        const uint64_t c0 = f2_pack(c[0], c[1]), c1 = f2_pack(c[2], c[3]), s0 = f2_pack(s[0], s[1]), s1 = f2_pack(s[2], s[3]);
+        const uint64_t rx0 = f2_sub(f2_mul(x0, c0), f2_mul(y0, s0)), rx1 = f2_sub(f2_mul(x1, c1), f2_mul(y1, s1));
+        y0 = f2_fma(x0, s0, f2_mul(y0, c0));
+        y1 = f2_fma(x1, s1, f2_mul(y1, c1));
+        x0 = rx0;
+        x1 = rx1;
+      }
+#pragma unroll
+      for (int h = 0; h < GP; ++h) {
+        const uint64_t t = f2_fma(q2[h][0], x0, f2_fma(q2[h][1], x1, f2_fma(q2[h][2], y0, f2_mul(q2[h][3], y1))));
+        float lo, hi;
+        f2_unpack(t, lo, hi);
+        val[n * GP + h] = lo + hi;
+      }
+    }
+    // reduce over the LPK lanes: each halving step hands half of the values to the partner lane
+    {
+      int cnt = NV;
+#pragma unroll
+      for (int mask = LPK / 2; mask > 0; mask >>= 1) {
+        if (cnt > 1) {
+          const bool up = ll & mask;
+#pragma unroll
+          for (int i = 0; i < NV / 2; ++i)
+            if (i < cnt / 2) {
+              const float send = up ? val[i] : val[i + cnt / 2], keep = up ? val[i + cnt / 2] : val[i];
+              val[i] = keep + __shfl_xor_sync(0xffffffffu, send, mask);
+            }
+          cnt >>= 1;
+        } else {
+          val[0] += __shfl_xor_sync(0xffffffffu, val[0], mask);
+        }
+      }
+    }
+    // this lane's own scores: key n = idx / GP, head idx % GP
+    bool grew = false;
+    float alpha[OWN];
+#pragma unroll
+    for (int u = 0; u < OWN; ++u) {
+      const int n = (own0 + u) / GP, h = (own0 + u) % GP, slot = base + n * KPW + kg;
+      const bool near = __shfl_sync(0xffffffffu, static_cast<int>(is_local), n * KPW + kg);
+      if (slot >= s_end || (a.window && !near)) val[u] = -INFINITY;
+      if (a.scores && slot < s_end && h < g && first_copy)
+        a.scores[(static_cast<long long>(b) * a.hq + kvh * g + h) * a.pitch + slot] = val[u];
+      float mx = val[u];
+#pragma unroll
+      for (int mask = 1; mask < 32; mask <<= 1)
+        if (!head_bit(mask)) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, mask));
+      const float m_new = fmaxf(m_own[u], mx);
+      alpha[u] = m_new == -INFINITY ? 1.f : fast_exp2(m_own[u] - m_new);
+      grew |= m_new > m_own[u];
+      m_own[u] = m_new;
+      const float p = val[u] == -INFINITY ? 0.f : fast_exp2(val[u] - m_new);
+      l_own[u] = l_own[u] * alpha[u] + p;
+      if (first_copy) sp[warp][kg][own0 + u] = p;
+    }
+    if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+      for (int h = 0; h < GP; ++h) {
+        const float f = __shfl_sync(0xffffffffu, alpha[h % OWN], h * LPK / NV);
+        const uint64_t f2 = f2_pack(f, f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o2[h][e] = f2_mul(o2[h][e], f2);
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int n = 0; n < NK; ++n) {
+      const uint64_t v0 = bf16x2_to_f2(v[n].x), v1 = bf16x2_to_f2(v[n].y), v2 = bf16x2_to_f2(v[n].z), v3 = bf16x2_to_f2(v[n].w);
+#pragma unroll
+      for (int h = 0; h < GP; ++h) {
+        const float p = sp[warp][kg][n * GP + h];
+        const uint64_t p2 = f2_pack(p, p);
+        o2[h][0] = f2_fma(p2, v0, o2[h][0]);
+        o2[h][1] = f2_fma(p2, v1, o2[h][1]);
+        o2[h][2] = f2_fma(p2, v2, o2[h][2]);
+        o2[h][3] = f2_fma(p2, v3, o2[h][3]);
+      }
+    }
+    __syncwarp();  // sp is rewritten by the next chunk
+  }
+
+  // merge: lane groups by shuffles, warps through shared memory in a fixed order
+#pragma unroll
+  for (int u = 0; u < OWN; ++u) {
+    float l = first_copy ? l_own[u] : 0.f;
+#pragma unroll
+    for (int mask = 1; mask < 32; mask <<= 1)
+      if (!head_bit(mask)) l += __shfl_xor_sync(0xffffffffu, l, mask);
+    if (own0 + u < GP && kg == 0 && first_copy) {
+      sm[warp][own0 + u] = m_own[u];
+      sl[warp][own0 + u] = l;
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < GP; ++h) {
+    float o[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f2_unpack(o2[h][e], o[2 * e], o[2 * e + 1]);
+#pragma unroll
+    for (int mask = LPK; mask < 32; mask <<= 1)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] += __shfl_xor_sync(0xffffffffu, o[e], mask);
+    if (kg == 0) {
+      *reinterpret_cast<float4*>(&so[warp][h][8 * ll]) = make_float4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<float4*>(&so[warp][h][8 * ll + 4]) = make_float4(o[4], o[5], o[6], o[7]);
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < g * D; i += WARPS * 32) {
+    const int h = i / D, d = i % D;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sm[w][h]);
+    float acc = 0.f, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float f = sm[w][h] == -INFINITY ? 0.f : fast_exp2(sm[w][h] - M);
+      acc += so[w][h][d] * f;
+      l += sl[w][h] * f;
+    }
+    const long long part = (static_cast<long long>(b) * a.hq + kvh * g + h) * a.n_split + split;
+    a.part_o[part * D + d] = acc;
+    if (d == 0) {
+      a.part_ml[part * 2] = M;
+      a.part_ml[part * 2 + 1] = l;
+    }
+  }
+}
+
+// Merges the ranges' partial results and adds the weights. CTA (x, kv head, sequence): every CTA forms
+// the log-sum-exps of the head's group from the partial maxima and sums (a few hundred bytes); x = 0
+// writes out and lse, and each x the weights of its SLOTS slots.
+constexpr int KEPT_FINISH_THREADS = 256, KEPT_FINISH_SLOTS = 1024;
+
+template <int D>
+__global__ void __launch_bounds__(KEPT_FINISH_THREADS) decode_kept_finish_kernel(const __grid_constant__ KeptArgs a) {
+  __shared__ float s_lse2[kept::MAX_G];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int kvh = blockIdx.y, b = blockIdx.z, g = a.hq / a.hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const KeptSeq seq = kept_seq(a, b);
+  if (!seq.ok) {
+    if (blockIdx.x == 0)
+      for (int i = threadIdx.x; i < g * D; i += KEPT_FINISH_THREADS) {
+        const long long h = static_cast<long long>(b) * a.hq + kvh * g + i / D;
+        a.out[h * D + i % D] = __float2bfloat16(__int_as_float(0x7fc00000));
+        if (a.lse && i % D == 0) a.lse[h] = __int_as_float(0x7fc00000);
+      }
+    return;
+  }
+  const int beg = blockIdx.x * KEPT_FINISH_SLOTS;
+  if (blockIdx.x > 0 && beg >= seq.n) return;
+  const int n_split = (seq.n + a.split_len - 1) / a.split_len;
+  if (warp < g) {
+    const float* ml = a.part_ml + (static_cast<long long>(b) * a.hq + kvh * g + warp) * a.n_split * 2;
+    float m = -INFINITY, l = 0.f;
+    for (int i = lane; i < n_split; i += 32) {
+      const float mi = ml[2 * i], M = fmaxf(m, mi);
+      if (M > -INFINITY) l = l * fast_exp2(m - M) + ml[2 * i + 1] * fast_exp2(mi - M);
+      m = M;
+    }
+#pragma unroll
+    for (int mask = 16; mask > 0; mask >>= 1) {
+      const float mo = __shfl_xor_sync(0xffffffffu, m, mask), lo = __shfl_xor_sync(0xffffffffu, l, mask);
+      const float M = fmaxf(m, mo);
+      if (M > -INFINITY) l = l * fast_exp2(m - M) + lo * fast_exp2(mo - M);
+      m = M;
+    }
+    if (lane == 0) s_lse2[warp] = m + log2f(l);
+  }
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    for (int i = threadIdx.x; i < g * D; i += KEPT_FINISH_THREADS) {
+      const int h = i / D, d = i % D;
+      const long long head = static_cast<long long>(b) * a.hq + kvh * g + h;
+      float acc = 0.f;
+      for (int sp = 0; sp < n_split; ++sp)
+        acc += a.part_o[(head * a.n_split + sp) * D + d] * fast_exp2(a.part_ml[(head * a.n_split + sp) * 2] - s_lse2[h]);
+      a.out[head * D + d] = __float2bfloat16(acc);
+      if (a.lse && d == 0) a.lse[head] = s_lse2[h] * 0.69314718055994530942f;
+    }
+  }
+  if (!a.kweight) return;
+  const int end = min(seq.n, beg + KEPT_FINISH_SLOTS);
+  for (int slot = beg + threadIdx.x; slot < end; slot += KEPT_FINISH_THREADS) {
+    const long long r = cache_row(a.rows, b, slot, 0);
+    if (r < 0) continue;
+    float w = 0.f;
+    for (int h = 0; h < g; ++h)
+      w += fast_exp2(a.scores[(static_cast<long long>(b) * a.hq + kvh * g + h) * a.pitch + slot] - s_lse2[h]);
+    float* dst = a.kweight + static_cast<long long>(kvh) * a.rows.rows + r;
+    *dst = slot == seq.n - 1 ? w : *dst + w;  // the new token's slot starts at zero
+  }
+}
+
+}  // namespace bf

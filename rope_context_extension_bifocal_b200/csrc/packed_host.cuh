@@ -232,6 +232,212 @@ bf_status_t prefill_packed_impl(const void* q, const void* k, const void* v, int
   return e == cudaSuccess ? BF_OK : BF_ERR_CUDA;
 }
 
+// ------------------------------------------------------------------ decode over kept slots
+struct KeptLayout {
+  size_t part_o, part_ml, scores, total;
+  int n_split, split_len, pitch;
+};
+
+// Ranges of slots: about 1024 CTAs in all (seven of 128 threads on each SM) as long as a range keeps 64
+// slots, and never more than 1024 slots in one, so that a batch of unequal lengths fills the GPU evenly.
+KeptLayout kept_layout(int batch, int max_len, bool accumulate, const bf_params_t* p) {
+  KeptLayout w{};
+  const int64_t segs = static_cast<int64_t>(batch) * p->hkv;
+  int64_t n = std::max<int64_t>((1024 + segs - 1) / segs, (static_cast<int64_t>(max_len) + 1023) / 1024);
+  n = std::min<int64_t>(n, (static_cast<int64_t>(max_len) + 63) / 64);
+  int64_t len = (max_len + n - 1) / n;
+  len = (len + 63) / 64 * 64;
+  w.split_len = static_cast<int>(len);
+  w.n_split = static_cast<int>((max_len + len - 1) / len);
+  w.pitch = static_cast<int>(std::min<int64_t>((static_cast<int64_t>(max_len) + 7) / 8 * 8, 0x7fffffff));
+  const size_t rows = static_cast<size_t>(batch) * p->hq;
+  w.part_ml = align256(rows * w.n_split * p->head_dim * 4);
+  w.scores = w.part_ml + align256(rows * w.n_split * 2 * 4);
+  w.total = w.scores + (accumulate ? align256(rows * w.pitch * 4) : 0);
+  return w;
+}
+
+bf_status_t check_kept(int32_t batch, int32_t max_len, const bf_params_t* p) {
+  const bf_status_t s = check_params(p, true);
+  if (s != BF_OK) return s;
+  if (batch < 1 || max_len < 1) return BF_ERR_INVALID;
+  if ((p->flags & BF_FLAG_WINDOW) && p->w0 < 1) return BF_ERR_INVALID;
+  if (p->hq / p->hkv > bf::kept::MAX_G || batch > 65535 || p->hkv > 65535) return BF_ERR_UNSUPPORTED;
+  return BF_OK;
+}
+
+template <int D>
+cudaError_t launch_kept(const bf::KeptArgs& a, int batch, cudaStream_t st) {
+  const dim3 grid(a.n_split, a.hkv, batch), block(bf::kept::WARPS * 32);
+  const int g = a.hq / a.hkv;
+  cudaError_t e = g == 1   ? launch_pdl(bf::decode_kept_kernel<D, 1>, grid, block, 0, st, a)
+                  : g == 2 ? launch_pdl(bf::decode_kept_kernel<D, 2>, grid, block, 0, st, a)
+                  : g <= 4 ? launch_pdl(bf::decode_kept_kernel<D, 4>, grid, block, 0, st, a)
+                           : launch_pdl(bf::decode_kept_kernel<D, 8>, grid, block, 0, st, a);
+  if (e != cudaSuccess) return e;
+  const int64_t chunks = a.kweight ? (static_cast<int64_t>(a.max_len) + bf::KEPT_FINISH_SLOTS - 1) / bf::KEPT_FINISH_SLOTS : 1;
+  return launch_pdl(bf::decode_kept_finish_kernel<D>, dim3(static_cast<unsigned>(chunks), a.hkv, batch),
+                    dim3(bf::KEPT_FINISH_THREADS), 0, st, a);
+}
+
+bf_status_t decode_kept_impl(const void* q, const void* k_new, const void* v_new, void* kcache, void* vcache,
+                             int32_t* kpos, float* kweight, int64_t cache_rows, int32_t page_size,
+                             const int32_t* block_table, int32_t max_pages, const int32_t* seq_lens,
+                             const int32_t* positions, int32_t max_len, int32_t batch, const bf_params_t* p, void* out,
+                             float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  bf_status_t s = check_kept(batch, max_len, p);
+  if (s != BF_OK) return s;
+  if (!q || !k_new || !v_new || !kcache || !vcache || !kpos || !block_table || !seq_lens || !positions || !out)
+    return BF_ERR_INVALID;
+  if (!aligned(q, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(kcache, 16) || !aligned(vcache, 16) ||
+      !aligned(kpos, 4) || !aligned(seq_lens, 4) || !aligned(positions, 4) || !aligned(out, 16) ||
+      (kweight && !aligned(kweight, 4)) || (lse && !aligned(lse, 4)))
+    return BF_ERR_INVALID;
+  bf::KeptArgs a{};
+  s = make_cache_rows(cache_rows, page_size, block_table, max_pages, &a.rows);
+  if (s != BF_OK) return s;
+  if (static_cast<int64_t>(max_pages) * page_size < max_len) return BF_ERR_INVALID;
+  const KeptLayout lay = kept_layout(batch, max_len, kweight != nullptr, p);
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < lay.total) return BF_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const Rope rope = make_rope(p->rope_theta, p->head_dim, 1);
+  a.q = static_cast<const bf16*>(q);
+  a.k_new = static_cast<const bf16*>(k_new);
+  a.v_new = static_cast<const bf16*>(v_new);
+  a.kcache = static_cast<bf16*>(kcache);
+  a.vcache = static_cast<bf16*>(vcache);
+  a.kpos = kpos;
+  a.kweight = kweight;
+  a.seq_lens = seq_lens;
+  a.positions = positions;
+  a.hq = p->hq;
+  a.hkv = p->hkv;
+  a.w0 = p->w0;
+  a.w_pretrained = p->w_pretrained;
+  a.mode = p->mode;
+  a.window = (p->flags & BF_FLAG_WINDOW) ? 1 : 0;
+  a.max_len = max_len;
+  a.split_len = lay.split_len;
+  a.n_split = lay.n_split;
+  a.scale_log2 = scale_log2(p);
+  a.part_o = reinterpret_cast<float*>(ws);
+  a.part_ml = reinterpret_cast<float*>(ws + lay.part_ml);
+  a.scores = kweight ? reinterpret_cast<float*>(ws + lay.scores) : nullptr;
+  a.pitch = lay.pitch;
+  a.out = static_cast<bf16*>(out);
+  a.lse = lse;
+  std::memcpy(a.omega, rope.omega, sizeof(a.omega));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = p->head_dim == 128 ? launch_kept<128>(a, batch, st) : launch_kept<64>(a, batch, st);
+  return e == cudaSuccess ? BF_OK : BF_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ eviction
+struct EvictLayout {
+  size_t lens, from, to, total;
+  int pitch;
+};
+
+EvictLayout evict_layout(int batch, int hkv, int max_len, int budget, bool in_place) {
+  EvictLayout w{};
+  const size_t segs = static_cast<size_t>(batch) * hkv;
+  w.pitch = std::min(max_len, budget);
+  const size_t list = align256(segs * w.pitch * 4);
+  w.lens = align256(segs * 4);
+  w.from = w.lens + align256(static_cast<size_t>(batch) * 4);
+  w.to = w.from + list;
+  w.total = w.to + (in_place ? list : 0);
+  return w;
+}
+
+bf_status_t check_evict(int32_t batch, int32_t hkv, int32_t head_dim, int32_t max_len, int32_t budget) {
+  if (batch < 1 || hkv < 1 || max_len < 1 || budget < 1) return BF_ERR_INVALID;
+  if ((head_dim != 64 && head_dim != 128) || batch > 65535 || hkv > 65535) return BF_ERR_UNSUPPORTED;
+  return BF_OK;
+}
+
+bf_status_t cache_evict_impl(void* kcache, void* vcache, int32_t* kpos, float* kweight, int64_t cache_rows,
+                             int32_t page_size, const int32_t* block_table, int32_t max_pages,
+                             const int32_t* dst_block_table, int32_t dst_max_pages, const int32_t* seq_lens,
+                             const int32_t* positions, int32_t* new_lens, int32_t batch, int32_t hkv, int32_t head_dim,
+                             int32_t max_len, int32_t budget, int32_t recent, int32_t sink, void* workspace,
+                             size_t ws_bytes, void* stream) {
+  bf_status_t s = check_evict(batch, hkv, head_dim, max_len, budget);
+  if (s != BF_OK) return s;
+  if (!kcache || !vcache || !kpos || !kweight || !block_table || !seq_lens || !positions || !new_lens)
+    return BF_ERR_INVALID;
+  if (recent < 0 || sink < 0 || static_cast<int64_t>(recent) + sink > budget) return BF_ERR_INVALID;
+  if (!aligned(kcache, 16) || !aligned(vcache, 16) || !aligned(kpos, 4) || !aligned(kweight, 4) ||
+      !aligned(seq_lens, 4) || !aligned(positions, 4) || !aligned(new_lens, 4))
+    return BF_ERR_INVALID;
+  bf::EvictArgs a{};
+  s = make_cache_rows(cache_rows, page_size, block_table, max_pages, &a.src);
+  if (s != BF_OK) return s;
+  if (static_cast<int64_t>(max_pages) * page_size < max_len) return BF_ERR_INVALID;
+  a.in_place = dst_block_table ? 0 : 1;
+  a.dst = a.src;
+  const EvictLayout lay = evict_layout(batch, hkv, max_len, budget, a.in_place != 0);
+  if (dst_block_table) {
+    s = make_cache_rows(cache_rows, page_size, dst_block_table, dst_max_pages, &a.dst);
+    if (s != BF_OK) return s;
+    if (static_cast<int64_t>(dst_max_pages) * page_size < lay.pitch) return BF_ERR_INVALID;
+  }
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < lay.total) return BF_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.kcache = static_cast<bf16*>(kcache);
+  a.vcache = static_cast<bf16*>(vcache);
+  a.kpos = kpos;
+  a.kweight = kweight;
+  a.seq_lens = seq_lens;
+  a.positions = positions;
+  a.new_lens = new_lens;
+  a.hkv = hkv;
+  a.max_len = max_len;
+  a.budget = budget;
+  a.recent = recent;
+  a.sink = sink;
+  a.moves = reinterpret_cast<int*>(ws);
+  a.lens = reinterpret_cast<int*>(ws + lay.lens);
+  a.from = reinterpret_cast<int*>(ws + lay.from);
+  a.to = reinterpret_cast<int*>(ws + (a.in_place ? lay.to : lay.from));
+  a.pitch = lay.pitch;
+  // a CTA for up to 4096 slots, a cluster of up to 8 for more
+  const int size = max_len <= 4096 ? 1 : max_len <= 8192 ? 2 : max_len <= 16384 ? 4 : 8;
+  // the slots of a CTA as the kernel divides them
+  const int64_t per_cta = ((static_cast<int64_t>(max_len) + size * bf::ev::WARPS - 1) / (size * bf::ev::WARPS) + 31) / 32 *
+                          32 * bf::ev::WARPS;
+  a.keys_in_smem = static_cast<int>(std::min<int64_t>(per_cta, bf::ev::MAX_RESIDENT));
+  const int smem = a.keys_in_smem * 4;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaFuncSetAttribute(bf::evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       bf::ev::MAX_RESIDENT * 4);
+  if (e != cudaSuccess) return BF_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(size, hkv, batch);
+  cfg.blockDim = dim3(bf::ev::THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = size;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, bf::evict_select_kernel, a);
+  if (e != cudaSuccess) return BF_ERR_CUDA;
+  // rows to move: a warp per 4 (D = 128) or 8 rows, about 2048 CTAs at most
+  const int64_t segs = static_cast<int64_t>(batch) * hkv;
+  const int rows_per_cta = 8 * 4 * (head_dim == 128 ? 1 : 2);
+  const int64_t x = std::max<int64_t>(1, std::min<int64_t>((lay.pitch + rows_per_cta - 1) / rows_per_cta, (2048 + segs - 1) / segs));
+  const dim3 grid(static_cast<unsigned>(x), hkv, batch);
+  e = head_dim == 128 ? launch_pdl(bf::evict_move_kernel<128>, grid, dim3(256), 0, st, a)
+                      : launch_pdl(bf::evict_move_kernel<64>, grid, dim3(256), 0, st, a);
+  return e == cudaSuccess ? BF_OK : BF_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -248,6 +454,36 @@ bf_status_t bifocal_prefill_packed(const void* q, const void* k, const void* v, 
                                    int32_t max_pages, void* workspace, size_t ws_bytes, void* stream) {
   return prefill_packed_impl(q, k, v, dtype, total_rows, batch, cu_seqlens, max_len, p, out, lse, kcache, vcache, kpos,
                              cache_rows, page_size, block_table, max_pages, workspace, ws_bytes, stream);
+}
+
+size_t bifocal_decode_kept_workspace_size(int32_t batch, int32_t max_len, int32_t accumulate, const bf_params_t* p) {
+  if (check_kept(batch, max_len, p) != BF_OK) return 0;
+  return kept_layout(batch, max_len, accumulate != 0, p).total;
+}
+
+bf_status_t bifocal_decode_kept(const void* q, const void* k_new, const void* v_new, void* kcache, void* vcache,
+                                int32_t* kpos, float* kweight, int64_t cache_rows, int32_t page_size,
+                                const int32_t* block_table, int32_t max_pages, const int32_t* seq_lens,
+                                const int32_t* positions, int32_t max_len, int32_t batch, const bf_params_t* p,
+                                void* out, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  return decode_kept_impl(q, k_new, v_new, kcache, vcache, kpos, kweight, cache_rows, page_size, block_table, max_pages,
+                          seq_lens, positions, max_len, batch, p, out, lse, workspace, ws_bytes, stream);
+}
+
+size_t bifocal_cache_evict_workspace_size(int32_t batch, int32_t hkv, int32_t max_len, int32_t budget) {
+  if (check_evict(batch, hkv, 64, max_len, budget) != BF_OK) return 0;
+  return evict_layout(batch, hkv, max_len, budget, true).total;
+}
+
+bf_status_t bifocal_cache_evict(void* kcache, void* vcache, int32_t* kpos, float* kweight, int64_t cache_rows,
+                                int32_t page_size, const int32_t* block_table, int32_t max_pages,
+                                const int32_t* dst_block_table, int32_t dst_max_pages, const int32_t* seq_lens,
+                                const int32_t* positions, int32_t* new_lens, int32_t batch, int32_t hkv,
+                                int32_t head_dim, int32_t max_len, int32_t budget, int32_t recent, int32_t sink,
+                                void* workspace, size_t ws_bytes, void* stream) {
+  return cache_evict_impl(kcache, vcache, kpos, kweight, cache_rows, page_size, block_table, max_pages, dst_block_table,
+                          dst_max_pages, seq_lens, positions, new_lens, batch, hkv, head_dim, max_len, budget, recent,
+                          sink, workspace, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -59,3 +59,47 @@ def test_binding_refuses_cpu_and_strided_tensors(lib):
     with pytest.raises(bfl.BifocalError) as e:
         bfl.bifocal_prefill_packed(q, q, q, cu, 4, w0=1, w_pretrained=8, theta=1e6)
     assert e.value.status == INVALID
+
+
+def test_decode_kept_validation(lib):
+    f = lib.bifocal_decode_kept
+
+    def call(p=None, q=FAKE, kn=FAKE, kc=FAKE, vc=FAKE, kpos=FAKE, kw=FAKE, rows=160, page=16, table=FAKE, max_pages=5,
+             lens=FAKE, pos=FAKE, max_len=80, B=2, out=FAKE, lse=None, ws=FAKE, wsb=0):
+        return f(q, kn, FAKE, kc, vc, kpos, kw, rows, page, table, max_pages, lens, pos, max_len, B, ctypes.byref(p or params()),
+                 out, lse, ws, wsb, None)
+
+    assert call() == WORKSPACE and call(kw=None) == WORKSPACE and call(ws=None) == WORKSPACE
+    for bad in (dict(q=None), dict(kn=FAKE + 8), dict(kc=None), dict(vc=FAKE + 2), dict(kpos=None), dict(kpos=FAKE + 2),
+                dict(kw=FAKE + 2), dict(rows=0), dict(rows=161), dict(page=0), dict(table=None), dict(table=FAKE + 1),
+                dict(max_pages=4), dict(max_pages=0), dict(lens=None), dict(pos=None), dict(pos=FAKE + 2), dict(max_len=0),
+                dict(B=0), dict(out=None), dict(out=FAKE + 8), dict(lse=FAKE + 2), dict(p=params(w0=-1)),
+                dict(p=params(theta=0.5)), dict(p=params(flags=bfl.FLAG_WINDOW, w0=0))):
+        assert call(**bad) == INVALID, bad
+    for bad in (dict(p=params(head_dim=96)), dict(p=params(hq=72, hkv=8)), dict(B=65536)):
+        assert call(**bad) == UNSUPPORTED, bad
+    assert call(p=params(hq=64, hkv=8)) == WORKSPACE and call(p=params(flags=bfl.FLAG_WINDOW, w0=8)) == WORKSPACE
+    small = bfl.decode_kept_workspace_size(2, 80, False, params())
+    assert 0 < small < bfl.decode_kept_workspace_size(2, 80, True, params())
+    assert bfl.decode_kept_workspace_size(0, 80, True, params()) == 0
+
+
+def test_cache_evict_validation(lib):
+    f = lib.bifocal_cache_evict
+
+    def call(kc=FAKE, vc=FAKE, kpos=FAKE, kw=FAKE, rows=160, page=16, table=FAKE, max_pages=5, dst=None, dst_pages=0, lens=FAKE,
+             pos=FAKE, new=FAKE, B=2, hkv=8, D=128, max_len=80, budget=32, recent=8, sink=4, ws=FAKE, wsb=0):
+        return f(kc, vc, kpos, kw, rows, page, table, max_pages, dst, dst_pages, lens, pos, new, B, hkv, D, max_len, budget,
+                 recent, sink, ws, wsb, None)
+
+    assert call() == WORKSPACE and call(ws=None) == WORKSPACE and call(recent=28) == WORKSPACE
+    for bad in (dict(kc=None), dict(vc=FAKE + 8), dict(kpos=None), dict(kw=None), dict(kw=FAKE + 2), dict(rows=150),
+                dict(rows=1 << 32), dict(page=0), dict(table=None), dict(max_pages=4), dict(lens=None), dict(pos=None),
+                dict(new=None), dict(new=FAKE + 2), dict(B=0), dict(hkv=0), dict(max_len=0), dict(budget=0), dict(recent=-1),
+                dict(sink=-1), dict(recent=29), dict(recent=1 << 30, sink=1 << 30), dict(dst=FAKE, dst_pages=1),
+                dict(dst=FAKE + 2, dst_pages=2)):
+        assert call(**bad) == INVALID, bad
+    for bad in (dict(D=96), dict(B=65536), dict(hkv=65536)):
+        assert call(**bad) == UNSUPPORTED, bad
+    assert call(dst=FAKE, dst_pages=2) == WORKSPACE
+    assert bfl.cache_evict_workspace_size(2, 8, 80, 32) > 0 and bfl.cache_evict_workspace_size(2, 8, 80, 0) == 0
