@@ -312,6 +312,29 @@ BF_API bf_status_t bifocal_decode_paged(const void* q, const void* k_new, const 
                                         int32_t max_len, int32_t batch, const bf_params_t* p, void* out,
                                         float* lse, void* workspace, size_t ws_bytes, void* stream);
 
+/* Attention weight that the keys of a packed batch of prompts have received: for every kv head and key j of
+ * sequence b the sum, over the sequence's last `obs` queries i >= j and the query heads of the kv head, of
+ * exp(score(i, j) - lse_i). With obs >= max_len every query counts.
+ *   q, k [total_rows, hq / hkv, D] raw, dtype, cu_seqlens, max_len: as for bifocal_prefill_packed
+ *   lse  [hq, total_rows] fp32: as that call wrote it (only the last obs rows of each sequence are read)
+ *   obs  >= 1
+ *   kweight [hkv, cache_rows] fp32, written (not added to): at the packed rows (block_table NULL;
+ *          cache_rows >= total_rows) or at the rows the block table gives, as for bifocal_prefill_packed;
+ *          other places are left as they were
+ *   workspace / ws_bytes: >= bifocal_key_weights_workspace_size(batch, total_rows, max_len, obs, p), 256-byte aligned
+ *          (forms of the queries that count: four fp16 copies).
+ * Scores are formed from operands split in two fp16 parts (about 2^-21 relative), not from the single fp16
+ * operands of the prefill. Errors on the device as for bifocal_prefill_packed; |q| or |k| from 65520 on is
+ * reported as BF_ERR_RANGE. Flags: BF_FLAG_WINDOW drops the long-range pairs (any head_dim and group).
+ * Errors: as bifocal_prefill_packed; BF_ERR_INVALID also for NULL lse or kweight and obs < 1. */
+BF_API size_t bifocal_key_weights_workspace_size(int32_t batch, int32_t total_rows, int32_t max_len, int32_t obs,
+                                                 const bf_params_t* p);
+BF_API bf_status_t bifocal_key_weights(const void* q, const void* k, int32_t dtype, const float* lse,
+                                       int32_t total_rows, int32_t batch, const int32_t* cu_seqlens, int32_t max_len,
+                                       int32_t obs, const bf_params_t* p, float* kweight, int64_t cache_rows,
+                                       int32_t page_size, const int32_t* block_table, int32_t max_pages,
+                                       void* workspace, size_t ws_bytes, void* stream);
+
 /* Cuts the caches of a batch of sequences to `budget` slots each, by the attention weight their keys
  * have received (kweight, accumulated by bifocal_key_weights and bifocal_decode_kept), every kv head by its
  * own. A slot is a place of a sequence's cache: slot s of sequence b is pool row

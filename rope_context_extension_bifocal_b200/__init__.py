@@ -18,7 +18,7 @@ __all__ = [
     "bifocal_factor", "bifocal_prefill", "bifocal_prefill_rope", "bifocal_prefill_attention", "rope_causal_prefill", "bifocal_prefill_chunk_paged", "bifocal_decode", "bifocal_decode_noalloc", "rope_causal_decode",
     "prefill_workspace_size", "decode_workspace_size", "last_device_error", "build_info", "test_set_fault",
     "bifocal_prefill_packed", "prefill_packed_workspace_size", "bifocal_cache_evict", "cache_evict_workspace_size",
-    "bifocal_decode_kept", "decode_kept_workspace_size",
+    "bifocal_decode_kept", "decode_kept_workspace_size", "bifocal_key_weights", "key_weights_workspace_size",
     "STATUS_TIMEOUT", "STATUS_RANGE", "STATUS_INDEX", "FAULT_NONE", "FAULT_PREFILL_SKIP_FILL", "FAULT_DECODE_SKIP_STAGE",
 ]
 
@@ -102,6 +102,10 @@ def _lib() -> ctypes.CDLL:
         L.bifocal_prefill_packed.argtypes = [vp, vp, vp, i32, i32, i32, vp, i32, pp, vp, vp, vp, vp, vp, i64, i32, vp, i32,
                                              vp, sz, vp]
         L.bifocal_prefill_packed.restype = i32
+        L.bifocal_key_weights_workspace_size.argtypes = [i32, i32, i32, i32, pp]
+        L.bifocal_key_weights_workspace_size.restype = sz
+        L.bifocal_key_weights.argtypes = [vp, vp, i32, vp, i32, i32, vp, i32, i32, pp, vp, i64, i32, vp, i32, vp, sz, vp]
+        L.bifocal_key_weights.restype = i32
         L.bifocal_decode_kept_workspace_size.argtypes = [i32, i32, i32, pp]
         L.bifocal_decode_kept_workspace_size.restype = sz
         L.bifocal_decode_kept.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i32, vp, i32, vp, vp, i32, i32, pp, vp, vp, vp,
@@ -467,6 +471,46 @@ def bifocal_prefill_packed(q, k, v, cu_seqlens, max_len: int, *, w0: int, w_pret
             _ptr(kcache), _ptr(vcache), _ptr(kpos), rows, int(page_size), _ptr(block_table),
             0 if block_table is None else block_table.shape[1], _ptr(ws), ws.numel() * ws.element_size(), st), fn)
     return out, lse
+
+
+def key_weights_workspace_size(batch: int, total_rows: int, max_len: int, obs: int, params: Params) -> int:
+    return int(_lib().bifocal_key_weights_workspace_size(int(batch), int(total_rows), int(max_len), int(obs),
+                                                         ctypes.byref(params)))
+
+
+def bifocal_key_weights(q, k, lse, cu_seqlens, max_len: int, obs: int, *, w0: int, w_pretrained: int, theta: float,
+                        mode: str = FREQ_INTERP, scale: Optional[float] = None, flags: int = 0, kweight=None,
+                        page_size: int = 0, block_table=None, workspace=None, stream=None):
+    """Attention weight of every key of packed prompts, summed over the last `obs` queries of its sequence and the
+    heads of its group. q [T, Hq, D], k [T, Hkv, D] raw (bf16 or fp32) and lse [Hq, T] fp32 as bifocal_prefill_packed
+    took and returned them; kweight [Hkv, rows] fp32 is written at the packed rows, or through block_table [B,
+    max_pages] int32 and page_size (default: a new [Hkv, T], unspecified at rows of no sequence). Returns kweight."""
+    import torch
+    fn = "bifocal_key_weights"
+    dev = _operands(fn, q=q, k=k, lse=lse, cu_seqlens=cu_seqlens, kweight=kweight, block_table=block_table,
+                    workspace=workspace)
+    _expect(fn, "q", q, (-1, -1, -1))
+    T, hq, D = q.shape
+    dt = _dtype_code(q)
+    _expect(fn, "k", k, (T, -1, D), q.dtype)
+    hkv = k.shape[1]
+    _expect(fn, "lse", lse, (hq, T), torch.float32)
+    _expect(fn, "cu_seqlens", cu_seqlens, (-1,), torch.int32)
+    B = cu_seqlens.numel() - 1
+    _expect(fn, "kweight", kweight, (hkv, -1), torch.float32)
+    _expect(fn, "block_table", block_table, (B, -1), torch.int32)
+    if kweight is None and block_table is not None:
+        raise BifocalError(1, f"{fn}: block_table needs kweight")
+    obs = min(int(obs), int(max_len))
+    p = make_params(hq, hkv, D, w0, w_pretrained, theta, mode, scale, flags)
+    with _On(dev, stream) as st:
+        kweight = torch.empty(hkv, T, dtype=torch.float32, device=dev) if kweight is None else kweight
+        ws = _workspace(key_weights_workspace_size(B, T, max_len, obs, p), dev) if workspace is None else workspace
+        _check(_lib().bifocal_key_weights(
+            _ptr(q), _ptr(k), dt, _ptr(lse), T, B, _ptr(cu_seqlens), int(max_len), obs, ctypes.byref(p), _ptr(kweight),
+            kweight.shape[1], int(page_size), _ptr(block_table), 0 if block_table is None else block_table.shape[1],
+            _ptr(ws), ws.numel() * ws.element_size(), st), fn)
+    return kweight
 
 
 def cache_evict_workspace_size(batch: int, hkv: int, max_len: int, budget: int) -> int:

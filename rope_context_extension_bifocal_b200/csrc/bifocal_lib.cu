@@ -15,6 +15,7 @@
 #include "decode.cuh"
 #include "decode_kept.cuh"
 #include "evict.cuh"
+#include "key_weights.cuh"
 #include "packed.cuh"
 #include "prefill_mma.cuh"
 #include "prefill_tc.cuh"

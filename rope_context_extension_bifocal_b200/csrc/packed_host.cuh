@@ -438,6 +438,119 @@ bf_status_t cache_evict_impl(void* kcache, void* vcache, int32_t* kpos, float* k
   return e == cudaSuccess ? BF_OK : BF_ERR_CUDA;
 }
 
+// ------------------------------------------------------------------ attention weight of keys
+struct WeightLayout {
+  size_t tiles, qoff, forms, form_bytes, nl, total;
+  int64_t max_tiles, rows;  // rows: of the query forms, at most
+};
+
+WeightLayout weight_layout(int batch, int T, int obs, const bf_params_t* p) {
+  WeightLayout w{};
+  w.max_tiles = packed_max_tiles(T, batch);
+  w.rows = std::min<int64_t>(static_cast<int64_t>(T) + 3LL * batch, (static_cast<int64_t>(obs) + 3) * batch);
+  w.rows = (w.rows + 3) / 4 * 4;
+  w.tiles = 256;
+  w.qoff = w.tiles + align256(static_cast<size_t>(w.max_tiles) * sizeof(int2));
+  w.forms = w.qoff + align256((static_cast<size_t>(batch) + 1) * 4);
+  w.form_bytes = align256(static_cast<size_t>(w.rows) * p->hq * p->head_dim * 2);
+  w.nl = w.forms + 4 * w.form_bytes;
+  w.total = w.nl + align256((static_cast<size_t>(w.rows) + 128) * p->hq * 4);
+  return w;
+}
+
+// Operand forms [heads][rows][D] fp16, box (64, 128, 1), 128B swizzle.
+bool make_form_map(CUtensorMap* map, const void* base, int64_t rows, int heads, int D) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(heads)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(rows) * D * 2};
+  cuuint32_t box[3] = {64, 128, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename Tin, int D>
+cudaError_t launch_weights(const bf::WeightArgs& a, cudaStream_t st) {
+  cudaError_t e = launch_pdl(bf::weights_query_kernel<Tin, D>, dim3(static_cast<unsigned>((a.form_rows + 7LL) / 8)),
+                             dim3(256), 0, st, a);
+  if (e != cudaSuccess) return e;
+  constexpr int smem = bf::key_weights_smem_bytes<D>();
+  auto kern = bf::key_weights_kernel<Tin, D>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(a.max_tiles) * a.hkv), dim3(bf::kw::NTHREADS), smem, st, a);
+}
+
+bf_status_t key_weights_impl(const void* q, const void* k, int32_t dtype, const float* lse, int32_t total_rows,
+                             int32_t batch, const int32_t* cu_seqlens, int32_t max_len, int32_t obs,
+                             const bf_params_t* p, float* kweight, int64_t cache_rows, int32_t page_size,
+                             const int32_t* block_table, int32_t max_pages, void* workspace, size_t ws_bytes,
+                             void* stream) {
+  bf_status_t s = check_packed(dtype, batch, total_rows, max_len, p);
+  if (s != BF_OK) return s;
+  if (!q || !k || !lse || !cu_seqlens || !kweight || obs < 1) return BF_ERR_INVALID;
+  const size_t align_in = dtype == BF_DTYPE_FP32 ? 32 : 16;
+  if (!aligned(q, align_in) || !aligned(k, align_in) || !aligned(lse, 4) || !aligned(cu_seqlens, 4) ||
+      !aligned(kweight, 4))
+    return BF_ERR_INVALID;
+  bf::WeightArgs a;
+  std::memset(&a, 0, sizeof(a));
+  s = make_cache_rows(cache_rows, page_size, block_table, max_pages, &a.rows);
+  if (s != BF_OK) return s;
+  if (block_table ? static_cast<int64_t>(max_pages) * page_size < max_len : cache_rows < total_rows)
+    return BF_ERR_INVALID;
+  obs = std::min(obs, max_len);
+  const WeightLayout lay = weight_layout(batch, total_rows, obs, p);
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < lay.total) return BF_ERR_WORKSPACE;
+  if (lay.max_tiles * p->hkv > 0x7fffffffLL || lay.rows > 0x7ffffeffLL) return BF_ERR_UNSUPPORTED;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int D = p->head_dim;
+  auto* head = reinterpret_cast<bf::PlanHeader*>(ws);
+  auto* tiles = reinterpret_cast<int2*>(ws + lay.tiles);
+  int* qoff = reinterpret_cast<int*>(ws + lay.qoff);
+  CUtensorMap* maps[4] = {&a.qo_hi, &a.qo_lo, &a.ql_hi, &a.ql_lo};
+  for (int i = 0; i < 4; ++i) {
+    a.forms[i] = reinterpret_cast<__half*>(ws + lay.forms + i * lay.form_bytes);
+    if (!make_form_map(maps[i], a.forms[i], lay.rows, p->hq, D)) return BF_ERR_CUDA;
+  }
+  if (launch_plan(cu_seqlens, batch, total_rows, max_len, obs, head, tiles, static_cast<int>(lay.max_tiles), qoff, st) !=
+      cudaSuccess)
+    return BF_ERR_CUDA;
+  const Rope rope = make_rope(p->rope_theta, D, 1);
+  a.q = q;
+  a.k = k;
+  a.lse = lse;
+  a.cu = cu_seqlens;
+  a.head = head;
+  a.tiles = tiles;
+  a.qoff = qoff;
+  a.batch = batch;
+  a.total_rows = total_rows;
+  a.hq = p->hq;
+  a.hkv = p->hkv;
+  a.max_tiles = static_cast<int>(lay.max_tiles);
+  a.obs = obs;
+  a.w0 = p->w0;
+  a.w_pretrained = p->w_pretrained;
+  a.mode = p->mode;
+  a.window = (p->flags & BF_FLAG_WINDOW) ? 1 : 0;
+  a.nl = reinterpret_cast<float*>(ws + lay.nl);
+  a.form_rows = static_cast<int>(lay.rows);
+  a.nl_pitch = static_cast<int>(lay.rows) + 128;
+  a.scale_log2 = scale_log2(p);
+  a.kweight = kweight;
+  std::memcpy(a.omega, rope.omega, sizeof(a.omega));
+  cudaError_t e;
+  if (dtype == BF_DTYPE_BF16)
+    e = D == 128 ? launch_weights<bf16, 128>(a, st) : launch_weights<bf16, 64>(a, st);
+  else
+    e = D == 128 ? launch_weights<float, 128>(a, st) : launch_weights<float, 64>(a, st);
+  return e == cudaSuccess ? BF_OK : BF_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -484,6 +597,21 @@ bf_status_t bifocal_cache_evict(void* kcache, void* vcache, int32_t* kpos, float
   return cache_evict_impl(kcache, vcache, kpos, kweight, cache_rows, page_size, block_table, max_pages, dst_block_table,
                           dst_max_pages, seq_lens, positions, new_lens, batch, hkv, head_dim, max_len, budget, recent,
                           sink, workspace, ws_bytes, stream);
+}
+
+size_t bifocal_key_weights_workspace_size(int32_t batch, int32_t total_rows, int32_t max_len, int32_t obs,
+                                          const bf_params_t* p) {
+  if (check_packed(BF_DTYPE_BF16, batch, total_rows, max_len, p) != BF_OK || obs < 1) return 0;
+  return weight_layout(batch, total_rows, std::min(obs, max_len), p).total;
+}
+
+bf_status_t bifocal_key_weights(const void* q, const void* k, int32_t dtype, const float* lse, int32_t total_rows,
+                                int32_t batch, const int32_t* cu_seqlens, int32_t max_len, int32_t obs,
+                                const bf_params_t* p, float* kweight, int64_t cache_rows, int32_t page_size,
+                                const int32_t* block_table, int32_t max_pages, void* workspace, size_t ws_bytes,
+                                void* stream) {
+  return key_weights_impl(q, k, dtype, lse, total_rows, batch, cu_seqlens, max_len, obs, p, kweight, cache_rows, page_size,
+                          block_table, max_pages, workspace, ws_bytes, stream);
 }
 
 }  // extern "C"

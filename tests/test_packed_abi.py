@@ -103,3 +103,26 @@ def test_cache_evict_validation(lib):
         assert call(**bad) == UNSUPPORTED, bad
     assert call(dst=FAKE, dst_pages=2) == WORKSPACE
     assert bfl.cache_evict_workspace_size(2, 8, 80, 32) > 0 and bfl.cache_evict_workspace_size(2, 8, 80, 0) == 0
+
+
+def test_key_weights_validation(lib):
+    f = lib.bifocal_key_weights
+
+    def call(p=None, q=FAKE, k=FAKE, dtype=0, lse=FAKE, T=100, B=3, cu=FAKE, max_len=60, obs=16, kw=FAKE, rows=100, page=0,
+             table=None, max_pages=0, ws=FAKE, wsb=0):
+        return f(q, k, dtype, lse, T, B, cu, max_len, obs, ctypes.byref(p or params()), kw, rows, page, table, max_pages, ws,
+                 wsb, None)
+
+    assert call() == WORKSPACE and call(ws=None) == WORKSPACE and call(obs=1 << 30) == WORKSPACE
+    assert call(p=params(hq=72, head_dim=64)) == WORKSPACE  # any group
+    assert call(rows=96, table=FAKE, page=24, max_pages=3) == WORKSPACE
+    for bad in (dict(q=None), dict(k=FAKE + 8), dict(lse=None), dict(lse=FAKE + 2), dict(T=0), dict(B=0), dict(cu=None),
+                dict(max_len=0), dict(obs=0), dict(kw=None), dict(kw=FAKE + 1), dict(rows=99), dict(rows=0),
+                dict(rows=96, table=FAKE, page=24, max_pages=2), dict(rows=97, table=FAKE, page=24, max_pages=3),
+                dict(p=params(w0=-1)), dict(p=params(flags=bfl.FLAG_WINDOW, w0=0))):
+        assert call(**bad) == INVALID, bad
+    for bad in (dict(dtype=3), dict(p=params(head_dim=32)), dict(p=params(flags=bfl.FLAG_MMA_SYNC))):
+        assert call(**bad) == UNSUPPORTED, bad
+    small = bfl.key_weights_workspace_size(3, 1000, 600, 16, params())
+    assert 0 < small < bfl.key_weights_workspace_size(3, 1000, 600, 600, params())
+    assert bfl.key_weights_workspace_size(3, 1000, 600, 0, params()) == 0
