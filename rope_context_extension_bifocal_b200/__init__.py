@@ -10,6 +10,7 @@ CPU fallback: without the built library every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -386,48 +387,62 @@ def rope_causal_decode(q, k_new, v_new, kcache, vcache, L: int, *, theta: float,
 # ---------------------------------------------------------------------------------------------
 # Packed prompts and cache eviction
 # ---------------------------------------------------------------------------------------------
-def _operands(where: str, **tensors):
-    """Checks the tensors of a call (None = not given): CUDA, one device, contiguous. Returns the device."""
+def _operands(where: str, *tensors):
+    """Checks the tensors of a call, given as (name, tensor or None, shape or None, type or None), where an entry -1 of a
+    shape is any size: CUDA, one device, contiguous, of that shape and type. Returns the device."""
     device = None
-    for name, t in tensors.items():
+    for name, t, shape, dtype in tensors:
         if t is None:
             continue
         if not t.is_cuda or not t.is_contiguous():
             raise BifocalError(1, f"{where}: {name} must be a contiguous CUDA tensor")
-        if device is not None and t.device != device:
+        if device is None:
+            device = t.device
+        elif t.device != device:
             raise BifocalError(1, f"{where}: {name} is on {t.device}, other tensors on {device}")
-        device = t.device
+        if dtype is not None and t.dtype is not dtype:
+            raise BifocalError(1, f"{where}: {name} has type {t.dtype}, expected {dtype}")
+        if shape is not None and t.shape != shape and (
+                t.dim() != len(shape) or any(w != -1 and n != w for n, w in zip(t.shape, shape))):
+            raise BifocalError(1, f"{where}: {name} has shape {tuple(t.shape)}, expected {shape}")
     return device
 
 
-def _expect(where: str, name: str, t, shape, *dtypes):
-    """Checks a tensor's shape (-1 = any) and type."""
-    if t is None:
-        return
-    if t.dim() != len(shape) or any(w != -1 and n != w for n, w in zip(t.shape, shape)):
-        raise BifocalError(1, f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if dtypes and t.dtype not in dtypes:
-        raise BifocalError(1, f"{where}: {name} has type {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-
-
 class _On:
-    """The device of a call's tensors made current, and the call's stream on it (default: that device's
-    current stream): what the call allocates belongs to that stream."""
+    """A call's stream (default: the current one of its tensors' device), made current with its device while the call
+    allocates and launches, so that what it allocates belongs to that stream."""
+    __slots__ = ("device", "stream", "guards")
 
     def __init__(self, device, stream):
-        import torch
-        self.guard = torch.cuda.device(device)
-        self.stream = torch.cuda.current_stream(device) if stream is None else stream
-        self.on = torch.cuda.stream(self.stream)
+        self.device, self.stream, self.guards = device, stream, ()
 
     def __enter__(self):
-        self.guard.__enter__()
-        self.on.__enter__()
-        return self.stream.cuda_stream
+        import torch
+        if self.stream is not None or self.device.index != torch.cuda.current_device():
+            guards = [torch.cuda.device(self.device)]
+            if self.stream is not None:
+                guards.append(torch.cuda.stream(self.stream))
+            for g in guards:
+                g.__enter__()
+            self.guards = guards
+        return torch.cuda.current_stream(self.device).cuda_stream if self.stream is None else self.stream.cuda_stream
 
     def __exit__(self, *exc):
-        self.on.__exit__(*exc)
-        return self.guard.__exit__(*exc)
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+@functools.lru_cache(maxsize=256)
+def _cached_params(hq, hkv, head_dim, w0, w_pretrained, theta, mode, scale, flags):
+    """The argument block of a call (read only) and a reference to it: a decode loop asks for the same one every step."""
+    p = make_params(hq, hkv, head_dim, w0, w_pretrained, theta, mode, scale, flags)
+    return p, ctypes.byref(p)
+
+
+@functools.lru_cache(maxsize=1024)
+def _cached_size(fn, *args):
+    """A workspace size: the same whenever the sizes are."""
+    return fn(*args)
 
 
 def prefill_packed_workspace_size(dtype: int, batch: int, total_rows: int, params: Params) -> int:
@@ -445,29 +460,27 @@ def bifocal_prefill_packed(q, k, v, cu_seqlens, max_len: int, *, w0: int, w_pret
     of no sequence are left as they were (in a new `out` or lse: unspecified)."""
     import torch
     fn = "bifocal_prefill_packed"
-    dev = _operands(fn, q=q, k=k, v=v, cu_seqlens=cu_seqlens, kcache=kcache, vcache=vcache, kpos=kpos,
-                    block_table=block_table, out=out, workspace=workspace)
-    _expect(fn, "q", q, (-1, -1, -1))
+    if q.dim() != 3 or k.dim() != 3:
+        raise BifocalError(1, f"{fn}: q and k must be [rows, heads, head_dim]")
     T, hq, D = q.shape
-    dt = _dtype_code(q)
-    _expect(fn, "k", k, (T, -1, D), q.dtype)
     hkv = k.shape[1]
-    _expect(fn, "v", v, (T, hkv, D), q.dtype)
-    _expect(fn, "cu_seqlens", cu_seqlens, (-1,), torch.int32)
+    dt = _dtype_code(q)
     B = cu_seqlens.numel() - 1
-    _expect(fn, "out", out, (T, hq, D), torch.bfloat16)
     rows = kcache.shape[0] if kcache is not None else 0
-    _expect(fn, "kcache", kcache, (rows, hkv, D), torch.bfloat16)
-    _expect(fn, "vcache", vcache, (rows, hkv, D), torch.bfloat16)
-    _expect(fn, "kpos", kpos, (hkv, rows), torch.int32)
-    _expect(fn, "block_table", block_table, (B, -1), torch.int32)
-    p = make_params(hq, hkv, D, w0, w_pretrained, theta, mode, scale, flags)
+    bf16, i32 = torch.bfloat16, torch.int32
+    dev = _operands(fn, ("q", q, None, None), ("k", k, (T, hkv, D), q.dtype), ("v", v, (T, hkv, D), q.dtype),
+                    ("cu_seqlens", cu_seqlens, (B + 1,), i32), ("out", out, (T, hq, D), bf16),
+                    ("kcache", kcache, (rows, hkv, D), bf16), ("vcache", vcache, (rows, hkv, D), bf16),
+                    ("kpos", kpos, (hkv, rows), i32), ("block_table", block_table, (B, -1), i32),
+                    ("workspace", workspace, None, None))
+    p, pref = _cached_params(hq, hkv, D, int(w0), int(w_pretrained), float(theta), mode,
+                             None if scale is None else float(scale), int(flags))
     with _On(dev, stream) as st:
-        out = torch.empty(T, hq, D, dtype=torch.bfloat16, device=dev) if out is None else out
+        out = torch.empty(T, hq, D, dtype=bf16, device=dev) if out is None else out
         lse = torch.empty(hq, T, dtype=torch.float32, device=dev) if want_lse else None
         ws = _workspace(prefill_packed_workspace_size(dt, B, T, p), dev) if workspace is None else workspace
         _check(_lib().bifocal_prefill_packed(
-            _ptr(q), _ptr(k), _ptr(v), dt, T, B, _ptr(cu_seqlens), int(max_len), ctypes.byref(p), _ptr(out), _ptr(lse),
+            _ptr(q), _ptr(k), _ptr(v), dt, T, B, _ptr(cu_seqlens), int(max_len), pref, _ptr(out), _ptr(lse),
             _ptr(kcache), _ptr(vcache), _ptr(kpos), rows, int(page_size), _ptr(block_table),
             0 if block_table is None else block_table.shape[1], _ptr(ws), ws.numel() * ws.element_size(), st), fn)
     return out, lse
@@ -487,27 +500,25 @@ def bifocal_key_weights(q, k, lse, cu_seqlens, max_len: int, obs: int, *, w0: in
     max_pages] int32 and page_size (default: a new [Hkv, T], unspecified at rows of no sequence). Returns kweight."""
     import torch
     fn = "bifocal_key_weights"
-    dev = _operands(fn, q=q, k=k, lse=lse, cu_seqlens=cu_seqlens, kweight=kweight, block_table=block_table,
-                    workspace=workspace)
-    _expect(fn, "q", q, (-1, -1, -1))
+    if q.dim() != 3 or k.dim() != 3:
+        raise BifocalError(1, f"{fn}: q and k must be [rows, heads, head_dim]")
     T, hq, D = q.shape
-    dt = _dtype_code(q)
-    _expect(fn, "k", k, (T, -1, D), q.dtype)
     hkv = k.shape[1]
-    _expect(fn, "lse", lse, (hq, T), torch.float32)
-    _expect(fn, "cu_seqlens", cu_seqlens, (-1,), torch.int32)
+    dt = _dtype_code(q)
     B = cu_seqlens.numel() - 1
-    _expect(fn, "kweight", kweight, (hkv, -1), torch.float32)
-    _expect(fn, "block_table", block_table, (B, -1), torch.int32)
     if kweight is None and block_table is not None:
         raise BifocalError(1, f"{fn}: block_table needs kweight")
+    dev = _operands(fn, ("q", q, None, None), ("k", k, (T, hkv, D), q.dtype), ("lse", lse, (hq, T), torch.float32),
+                    ("cu_seqlens", cu_seqlens, (B + 1,), torch.int32), ("kweight", kweight, (hkv, -1), torch.float32),
+                    ("block_table", block_table, (B, -1), torch.int32), ("workspace", workspace, None, None))
     obs = min(int(obs), int(max_len))
-    p = make_params(hq, hkv, D, w0, w_pretrained, theta, mode, scale, flags)
+    p, pref = _cached_params(hq, hkv, D, int(w0), int(w_pretrained), float(theta), mode,
+                             None if scale is None else float(scale), int(flags))
     with _On(dev, stream) as st:
         kweight = torch.empty(hkv, T, dtype=torch.float32, device=dev) if kweight is None else kweight
         ws = _workspace(key_weights_workspace_size(B, T, max_len, obs, p), dev) if workspace is None else workspace
         _check(_lib().bifocal_key_weights(
-            _ptr(q), _ptr(k), dt, _ptr(lse), T, B, _ptr(cu_seqlens), int(max_len), obs, ctypes.byref(p), _ptr(kweight),
+            _ptr(q), _ptr(k), dt, _ptr(lse), T, B, _ptr(cu_seqlens), int(max_len), obs, pref, _ptr(kweight),
             kweight.shape[1], int(page_size), _ptr(block_table), 0 if block_table is None else block_table.shape[1],
             _ptr(ws), ws.numel() * ws.element_size(), st), fn)
     return kweight
@@ -527,23 +538,19 @@ def bifocal_cache_evict(kcache, vcache, kpos, kweight, page_size: int, block_tab
     order. Returns new_lens [B] int32 = min(seq_lens, budget) (may be given; may be seq_lens)."""
     import torch
     fn = "bifocal_cache_evict"
-    dev = _operands(fn, kcache=kcache, vcache=vcache, kpos=kpos, kweight=kweight, block_table=block_table,
-                    seq_lens=seq_lens, positions=positions, dst_block_table=dst_block_table, new_lens=new_lens,
-                    workspace=workspace)
-    _expect(fn, "kcache", kcache, (-1, -1, -1), torch.bfloat16)
+    if kcache.dim() != 3:
+        raise BifocalError(1, f"{fn}: kcache must be [rows, kv heads, head_dim]")
     rows, hkv, D = kcache.shape
-    _expect(fn, "vcache", vcache, (rows, hkv, D), torch.bfloat16)
-    _expect(fn, "kpos", kpos, (hkv, rows), torch.int32)
-    _expect(fn, "kweight", kweight, (hkv, rows), torch.float32)
-    _expect(fn, "seq_lens", seq_lens, (-1,), torch.int32)
     B = seq_lens.numel()
-    _expect(fn, "positions", positions, (B,), torch.int32)
-    _expect(fn, "block_table", block_table, (B, -1), torch.int32)
-    _expect(fn, "dst_block_table", dst_block_table, (B, -1), torch.int32)
-    _expect(fn, "new_lens", new_lens, (B,), torch.int32)
+    bf16, i32 = torch.bfloat16, torch.int32
+    dev = _operands(fn, ("kcache", kcache, None, bf16), ("vcache", vcache, (rows, hkv, D), bf16),
+                    ("kpos", kpos, (hkv, rows), i32), ("kweight", kweight, (hkv, rows), torch.float32),
+                    ("block_table", block_table, (B, -1), i32), ("seq_lens", seq_lens, (B,), i32),
+                    ("positions", positions, (B,), i32), ("dst_block_table", dst_block_table, (B, -1), i32),
+                    ("new_lens", new_lens, (B,), i32), ("workspace", workspace, None, None))
     with _On(dev, stream) as st:
         new_lens = torch.empty_like(seq_lens) if new_lens is None else new_lens
-        ws = _workspace(cache_evict_workspace_size(B, hkv, max_len, budget), dev) if workspace is None else workspace
+        ws = _workspace(_cached_size(cache_evict_workspace_size, B, hkv, int(max_len), int(budget)), dev) if workspace is None else workspace
         _check(_lib().bifocal_cache_evict(
             _ptr(kcache), _ptr(vcache), _ptr(kpos), _ptr(kweight), rows, int(page_size), _ptr(block_table),
             block_table.shape[1], _ptr(dst_block_table), 0 if dst_block_table is None else dst_block_table.shape[1],
@@ -556,6 +563,10 @@ def decode_kept_workspace_size(batch: int, max_len: int, accumulate: bool, param
     return int(_lib().bifocal_decode_kept_workspace_size(int(batch), int(max_len), int(accumulate), ctypes.byref(params)))
 
 
+def _kept_size(batch, max_len, accumulate, hq, hkv, head_dim):
+    return decode_kept_workspace_size(batch, max_len, accumulate, make_params(hq, hkv, head_dim, 0, 1, 2.0))
+
+
 def bifocal_decode_kept(q, k_new, v_new, kcache, vcache, kpos, kweight, page_size: int, block_table, seq_lens, positions,
                         max_len: int, *, w0: int, w_pretrained: int, theta: float, mode: str = FREQ_INTERP,
                         scale: Optional[float] = None, flags: int = 0, want_lse: bool = True, out=None, workspace=None,
@@ -566,30 +577,29 @@ def bifocal_decode_kept(q, k_new, v_new, kcache, vcache, kpos, kweight, page_siz
     the device; max_len bounds seq_lens. Returns (out [B, Hq, D], lse [B, Hq] or None)."""
     import torch
     fn = "bifocal_decode_kept"
-    dev = _operands(fn, q=q, k_new=k_new, v_new=v_new, kcache=kcache, vcache=vcache, kpos=kpos, kweight=kweight,
-                    block_table=block_table, seq_lens=seq_lens, positions=positions, out=out, workspace=workspace)
-    _expect(fn, "q", q, (-1, -1, -1), torch.bfloat16)
+    if q.dim() != 3 or kcache.dim() != 3:
+        raise BifocalError(1, f"{fn}: q must be [batch, heads, head_dim] and kcache [rows, kv heads, head_dim]")
     B, hq, D = q.shape
-    _expect(fn, "kcache", kcache, (-1, -1, D), torch.bfloat16)
     rows, hkv, _ = kcache.shape
-    _expect(fn, "vcache", vcache, (rows, hkv, D), torch.bfloat16)
-    _expect(fn, "k_new", k_new, (B, hkv, D), torch.bfloat16)
-    _expect(fn, "v_new", v_new, (B, hkv, D), torch.bfloat16)
-    _expect(fn, "kpos", kpos, (hkv, rows), torch.int32)
-    _expect(fn, "kweight", kweight, (hkv, rows), torch.float32)
-    _expect(fn, "seq_lens", seq_lens, (B,), torch.int32)
-    _expect(fn, "positions", positions, (B,), torch.int32)
-    _expect(fn, "block_table", block_table, (B, -1), torch.int32)
-    _expect(fn, "out", out, (B, hq, D), torch.bfloat16)
-    p = make_params(hq, hkv, D, w0, w_pretrained, theta, mode, scale, flags)
+    bf16, i32 = torch.bfloat16, torch.int32
+    dev = _operands(fn, ("q", q, None, bf16), ("k_new", k_new, (B, hkv, D), bf16), ("v_new", v_new, (B, hkv, D), bf16),
+                    ("kcache", kcache, (rows, hkv, D), bf16), ("vcache", vcache, (rows, hkv, D), bf16),
+                    ("kpos", kpos, (hkv, rows), i32), ("kweight", kweight, (hkv, rows), torch.float32),
+                    ("block_table", block_table, (B, -1), i32), ("seq_lens", seq_lens, (B,), i32),
+                    ("positions", positions, (B,), i32), ("out", out, (B, hq, D), bf16),
+                    ("workspace", workspace, None, None))
+    p, pref = _cached_params(hq, hkv, D, int(w0), int(w_pretrained), float(theta), mode,
+                             None if scale is None else float(scale), int(flags))
     with _On(dev, stream) as st:
-        out = torch.empty(B, hq, D, dtype=torch.bfloat16, device=dev) if out is None else out
+        out = torch.empty(B, hq, D, dtype=bf16, device=dev) if out is None else out
         lse = torch.empty(B, hq, dtype=torch.float32, device=dev) if want_lse else None
-        ws = _workspace(decode_kept_workspace_size(B, max_len, kweight is not None, p), dev) if workspace is None else workspace
+        ws = workspace
+        if ws is None:
+            ws = _workspace(_cached_size(_kept_size, B, int(max_len), kweight is not None, hq, hkv, D), dev)
         _check(_lib().bifocal_decode_kept(
             _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(kcache), _ptr(vcache), _ptr(kpos), _ptr(kweight), rows,
             int(page_size), _ptr(block_table), block_table.shape[1], _ptr(seq_lens), _ptr(positions), int(max_len), B,
-            ctypes.byref(p), _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), st), fn)
+            pref, _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), st), fn)
     return out, lse
 
 

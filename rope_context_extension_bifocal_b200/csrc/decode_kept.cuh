@@ -33,6 +33,8 @@ namespace bf {
 namespace kept {
 constexpr int WARPS = 4;
 constexpr int NK = 4;       // keys a lane group holds at a time
+constexpr int STAGES = 3;   // stages of a warp's ring: two on their way while one is used
+constexpr int STAGE_BYTES = 4096;
 constexpr int MAX_G = 8;    // query heads per kv head (max)
 }  // namespace kept
 
@@ -45,6 +47,7 @@ struct KeptArgs {
   int* kpos;                   // [hkv, rows]
   float* kweight;              // [hkv, rows] or null
   CacheRows rows;
+  int page_shift;              // log2 of the page size, -1 when it is not a power of two
   const int* seq_lens;         // [B] slots with the new token's
   const int* positions;        // [B] position of the new token
   int hq, hkv, w0, w_pretrained, mode, window, max_len;
@@ -77,18 +80,29 @@ __device__ __forceinline__ KeptSeq kept_seq(const KeptArgs& a, int b) {
 
 __device__ __forceinline__ int far_multiple(int p, int G, int mode) { return mode == 0 ? p : p - p / G; }
 
+// Shared memory of a CTA: the warps' stages; reused for the merge at the end.
 template <int D, int GP>
-__global__ void __launch_bounds__(kept::WARPS * 32) decode_kept_kernel(const __grid_constant__ KeptArgs a) {
+constexpr int kept_smem_bytes() {
+  return kept::WARPS * kept::STAGES * kept::STAGE_BYTES > kept::WARPS * GP * D * 4 ? kept::WARPS * kept::STAGES * kept::STAGE_BYTES
+                                                                                 : kept::WARPS * GP * D * 4;
+}
+
+// Four CTAs on an SM for up to four heads (128 registers a thread), two for eight (their queries and
+// accumulators alone are 128).
+template <int D, int GP>
+__global__ void __launch_bounds__(kept::WARPS * 32, GP <= 4 ? 4 : 2) decode_kept_kernel(const __grid_constant__ KeptArgs a) {
   using namespace kept;
   constexpr int P = D / 2;
   constexpr int LPK = D / 8;        // lanes a key
   constexpr int KPW = 32 / LPK;     // keys side by side in a warp
-  constexpr int CH = NK * KPW;      // keys of a warp's chunk
+  constexpr int CH = NK * KPW;      // keys of a warp's stage
+  constexpr int SUB = 32 / CH;      // stages of a block of 32 slots
   constexpr int NV = NK * GP;       // scores a lane group reduces
   constexpr int OWN = NV > LPK ? NV / LPK : 1;  // of which a lane keeps this many
-  __shared__ __align__(16) float sp[WARPS][KPW][NV];
+  static_assert(CH * D * 4 == STAGE_BYTES, "a stage holds the keys and values of CH slots");
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ __align__(16) float2 sp[WARPS][KPW][NV];  // probabilities, twice each (packed operands)
   __shared__ float sm[WARPS][GP], sl[WARPS][GP];
-  __shared__ __align__(16) float so[WARPS][GP][D];
 
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -103,6 +117,52 @@ __global__ void __launch_bounds__(kept::WARPS * 32) decode_kept_kernel(const __g
   }
   const int s_beg = split * a.split_len, s_end = min(seq.n, s_beg + a.split_len);
   if (s_beg >= s_end) return;
+
+  // Row and position of this lane's slot of a block of 32 (row -1: past the range, or a bad page)
+  const int* trow = a.rows.block_table + static_cast<long long>(b) * a.rows.max_pages;
+  const int* kpos = a.kpos + static_cast<long long>(kvh) * a.rows.rows;
+  auto lookup = [&](int base, int& row, int& pos) {
+    const int slot = base + lane;
+    row = -1;
+    pos = seq.now;
+    if (slot < s_end) {
+      const int page = a.page_shift >= 0 ? slot >> a.page_shift : slot / a.rows.page_size;
+      const int pg = trow[page];
+      if (pg < 0 || pg >= a.rows.pool_pages) {
+        report_status(kDevIndex, 71);
+      } else {
+        row = pg * a.rows.page_size + (slot - page * a.rows.page_size);
+        if (slot != seq.n - 1) pos = kpos[row];
+      }
+    }
+  };
+  // One stage: the K and V rows of slots CH sub .. of the block whose rows are `row`, 16 bytes a lane. A copy of
+  // 32 lanes is one slot (D = 128: 16 lanes its key, 16 its value) or two.
+  uint8_t* stages = smem + warp * STAGES * STAGE_BYTES;
+  const uint32_t st0 = smem_u32(stages);
+  const int c_lane = lane % (D / 4), c_slot = lane / (D / 4);  // lane of a slot's D / 4 lanes, slot of the copy
+  const bool c_is_v = c_lane >= D / 8;
+  const __nv_bfloat16* c_src = (c_is_v ? a.vcache : a.kcache) + static_cast<long long>(kvh) * D + (c_lane % (D / 8)) * 8;
+  const long long c_stride = static_cast<long long>(a.hkv) * D;
+  constexpr int SPC = 128 / D;  // slots a copy
+  auto fill = [&](int stage, int row, int sub) {
+#pragma unroll
+    for (int i = 0; i < CH / SPC; ++i) {
+      const int r = __shfl_sync(0xffffffffu, row, sub * CH + i * SPC + c_slot);
+      cp_async_16(st0 + stage * STAGE_BYTES + i * 512 + lane * 16, c_src + (r >= 0 ? r * c_stride : 0), r >= 0);
+    }
+  };
+
+  int row, pos, nrow, npos;
+  int base = s_beg + warp * 32;
+  lookup(base, row, pos);
+  lookup(base + WARPS * 32, nrow, npos);
+  // two stages ahead of the one in use
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) {
+    if (i < SUB) fill(i, row, i); else fill(i, nrow, i - SUB);
+    cp_async_commit();
+  }
 
   // the query heads' rows under R_l(now) (R_o when nothing is long-range), in the log2 domain, and
   // the turn fractions of the correction: this lane's pairs 4 ll .. 4 ll + 3
@@ -122,7 +182,7 @@ __global__ void __launch_bounds__(kept::WARPS * 32) decode_kept_kernel(const __g
       t = (t - floor(t)) * 4294967296.0;
       const double hi = fmin(floor(t), 4294967295.0);
       whi[e] = static_cast<uint32_t>(hi);
-      wlo[e] = static_cast<float>((t - hi) * 2.3283064365386962890625e-10);
+      wlo[e] = static_cast<float>((t - hi) * (2.3283064365386962890625e-10 * 6.283185307179586476925286766559));
     }
 #pragma unroll
     for (int h = 0; h < GP; ++h) {
@@ -146,36 +206,6 @@ __global__ void __launch_bounds__(kept::WARPS * 32) decode_kept_kernel(const __g
   }
   const int m_now = far_multiple(seq.now, seq.G, a.mode);
 
-  // Row, position and validity of the chunk's key i = lane % CH (key n of lane group kg is i = n * KPW + kg)
-  auto lookup = [&](int base, int& row, int& pos) {
-    const int slot = base + lane % CH;
-    row = -1;
-    pos = seq.now;
-    if (slot < s_end) {
-      const long long r = cache_row(a.rows, b, slot, 0);
-      if (r < 0) {
-        report_status(kDevIndex, 71);
-      } else {
-        row = static_cast<int>(r);
-        if (slot != seq.n - 1) pos = a.kpos[static_cast<long long>(kvh) * a.rows.rows + row];
-      }
-    }
-  };
-  auto load = [&](int row, uint2 (&kx)[NK], uint2 (&ky)[NK], uint4 (&v)[NK]) {
-#pragma unroll
-    for (int n = 0; n < NK; ++n) {
-      const int r = __shfl_sync(0xffffffffu, row, n * KPW + kg);
-      kx[n] = ky[n] = make_uint2(0u, 0u);
-      v[n] = make_uint4(0u, 0u, 0u, 0u);
-      if (r >= 0) {
-        const long long at = (static_cast<long long>(r) * a.hkv + kvh) * D;
-        kx[n] = *reinterpret_cast<const uint2*>(a.kcache + at + 4 * ll);
-        ky[n] = *reinterpret_cast<const uint2*>(a.kcache + at + P + 4 * ll);
-        v[n] = *reinterpret_cast<const uint4*>(a.vcache + at + 8 * ll);
-      }
-    }
-  };
-
   uint64_t o2[GP][4];
 #pragma unroll
   for (int h = 0; h < GP; ++h)
@@ -190,30 +220,40 @@ __global__ void __launch_bounds__(kept::WARPS * 32) decode_kept_kernel(const __g
   for (int u = 0; u < OWN; ++u) m_own[u] = -INFINITY, l_own[u] = 0.f;
   // lane bits that select the head of a score; the others select the key or a copy
   auto head_bit = [](int mask) { return mask < LPK && mask * NV / LPK >= 1 && mask * NV / LPK < GP; };
+  float* score_at = a.scores ? a.scores + (static_cast<long long>(b) * a.hq + kvh * g) * a.pitch : nullptr;
 
-  uint2 kx[NK], ky[NK], nkx[NK], nky[NK];
-  uint4 v[NK], nv[NK];
-  int row, pos, nrow, npos;
-  int base = s_beg + warp * CH;
-  if (base < s_end) {
-    lookup(base, nrow, npos);
-    load(nrow, nkx, nky, nv);
-  }
-  for (; base < s_end; base += WARPS * CH) {
-    row = nrow;
-    pos = npos;
-#pragma unroll
-    for (int n = 0; n < NK; ++n) kx[n] = nkx[n], ky[n] = nky[n], v[n] = nv[n];
-    if (base + WARPS * CH < s_end) {
-      lookup(base + WARPS * CH, nrow, npos);
-      load(nrow, nkx, nky, nv);
-    }
-    // the new token's key and value: rotated, rounded to the cache's bf16, appended and used from there
-    if (base + CH >= seq.n && seq.n > base) {
+  int stage = 0;
+  for (; base < s_end; base += WARPS * 32) {
+    const bool is_local = seq.now - pos < a.w0;
+    const int mult = is_local ? m_now : far_multiple(pos, seq.G, a.mode);
+    const unsigned local_mask = __ballot_sync(0xffffffffu, is_local);
+#pragma unroll 1
+    for (int sub = 0; sub < SUB; ++sub) {
+      const int sbase = base + sub * CH;
+      if (sbase >= s_end) {  // warp-uniform: the rest of the last block
+        cp_async_commit();
+        stage = stage == STAGES - 1 ? 0 : stage + 1;
+        continue;
+      }
+      // two stages on: this block's, or the next one's first
+      {
+        const int ahead = sub + STAGES - 1, to = stage == 0 ? STAGES - 1 : stage - 1;
+        fill(to, ahead < SUB ? row : nrow, ahead % SUB);
+        cp_async_commit();
+      }
+      cp_async_wait<STAGES - 1>();
+      __syncwarp();
+      const uint8_t* st = stages + stage * STAGE_BYTES;
+      // scores: this lane's share of each (key, head), then the sum over the key's lanes
+      float val[NV];
 #pragma unroll
       for (int n = 0; n < NK; ++n) {
-        const int r = __shfl_sync(0xffffffffu, row, n * KPW + kg);
-        if (base + n * KPW + kg == seq.n - 1) {
+        const int i = n * KPW + kg;
+        uint8_t* kr = const_cast<uint8_t*>(st) + i * (D * 4);
+        uint2 kx = *reinterpret_cast<const uint2*>(kr + ll * 8), ky = *reinterpret_cast<const uint2*>(kr + D + ll * 8);
+        if (sbase + i == seq.n - 1) {
+          // the new token: its key rotated and rounded to the cache's bf16; key, value and position are
+          // appended, and used from here on as the cache holds them
           const long long src = (static_cast<long long>(b) * a.hkv + kvh) * D;
           const uint2 u = *reinterpret_cast<const uint2*>(a.k_new + src + 4 * ll);
           const uint2 w = *reinterpret_cast<const uint2*>(a.k_new + src + P + 4 * ll);
@@ -227,119 +267,120 @@ __global__ void __launch_bounds__(kept::WARPS * 32) decode_kept_kernel(const __g
             x[e] = xr[e] * c - yr[e] * s;
             y[e] = yr[e] * c + xr[e] * s;
           }
-          kx[n] = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-          ky[n] = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-          v[n] = *reinterpret_cast<const uint4*>(a.v_new + src + 8 * ll);
-          if (r >= 0) {
-            const long long at = (static_cast<long long>(r) * a.hkv + kvh) * D;
-            *reinterpret_cast<uint2*>(a.kcache + at + 4 * ll) = kx[n];
-            *reinterpret_cast<uint2*>(a.kcache + at + P + 4 * ll) = ky[n];
-            *reinterpret_cast<uint4*>(a.vcache + at + 8 * ll) = v[n];
+          kx = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+          ky = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+          const uint4 v = *reinterpret_cast<const uint4*>(a.v_new + src + 8 * ll);
+          *reinterpret_cast<uint4*>(kr + 2 * D + ll * 16) = v;  // read back below by this lane alone
+          const int page = (seq.n - 1) / a.rows.page_size, pg = trow[page];
+          if (pg >= 0 && pg < a.rows.pool_pages) {
+            const long long r = static_cast<long long>(pg) * a.rows.page_size + (seq.n - 1 - page * a.rows.page_size);
+            const long long at = (r * a.hkv + kvh) * D;
+            *reinterpret_cast<uint2*>(a.kcache + at + 4 * ll) = kx;
+            *reinterpret_cast<uint2*>(a.kcache + at + P + 4 * ll) = ky;
+            *reinterpret_cast<uint4*>(a.vcache + at + 8 * ll) = v;
             if (ll == 0) a.kpos[static_cast<long long>(kvh) * a.rows.rows + r] = seq.now;
           }
         }
-      }
-    }
-    // scores: this lane's share of each (key, head), then the sum over the key's lanes
-    const bool is_local = seq.now - pos < a.w0;
-    const int mult = is_local ? m_now : far_multiple(pos, seq.G, a.mode);
-    float val[NV];
+        uint64_t x0 = bf16x2_to_f2(kx.x), x1 = bf16x2_to_f2(kx.y), y0 = bf16x2_to_f2(ky.x), y1 = bf16x2_to_f2(ky.y);
+        if (seq.rot) {
+          const int m = __shfl_sync(0xffffffffu, mult, sub * CH + i);
+          const float mf = static_cast<float>(m);
+          float c[4], s[4];
 #pragma unroll
-    for (int n = 0; n < NK; ++n) {
-      uint64_t x0 = bf16x2_to_f2(kx[n].x), x1 = bf16x2_to_f2(kx[n].y);
-      uint64_t y0 = bf16x2_to_f2(ky[n].x), y1 = bf16x2_to_f2(ky[n].y);
-      if (seq.rot) {
-        const int m = __shfl_sync(0xffffffffu, mult, n * KPW + kg);
-        const float mf = static_cast<float>(m);
-        float c[4], s[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // turns in [-1/2, 1/2): the top bits of the wrapped product as the mantissa of a float in [1, 2)
-          const uint32_t ph = static_cast<uint32_t>(m) * whi[e] + 0x80000100u;
-          const float t = __uint_as_float((ph >> 9) | 0x3f800000u) - 1.5f;
-          __sincosf(fmaf(mf, wlo[e], t) * 6.283185307179586f, &s[e], &c[e]);
+          for (int e = 0; e < 4; ++e) {
+            // the wrapped product's top bits as the mantissa of f in [1, 2): f - 1.5 turns, in [-1/2, 1/2)
+            const uint32_t ph = static_cast<uint32_t>(m) * whi[e] + 0x80000100u;
+            const float f = __uint_as_float(__funnelshift_r(ph, 0x7fu, 9));
+            __sincosf(fmaf(f, 6.283185307179586f, fmaf(mf, wlo[e], -9.42477796076938f)), &s[e], &c[e]);
+          }
+          const uint64_t c0 = f2_pack(c[0], c[1]), c1 = f2_pack(c[2], c[3]), s0 = f2_pack(s[0], s[1]), s1 = f2_pack(s[2], s[3]);
+          const uint64_t rx0 = f2_sub(f2_mul(x0, c0), f2_mul(y0, s0)), rx1 = f2_sub(f2_mul(x1, c1), f2_mul(y1, s1));
+          y0 = f2_fma(x0, s0, f2_mul(y0, c0));
+          y1 = f2_fma(x1, s1, f2_mul(y1, c1));
+          x0 = rx0;
+          x1 = rx1;
         }
-        const uint64_t c0 = f2_pack(c[0], c[1]), c1 = f2_pack(c[2], c[3]), s0 = f2_pack(s[0], s[1]), s1 = f2_pack(s[2], s[3]);
-        const uint64_t rx0 = f2_sub(f2_mul(x0, c0), f2_mul(y0, s0)), rx1 = f2_sub(f2_mul(x1, c1), f2_mul(y1, s1));
-        y0 = f2_fma(x0, s0, f2_mul(y0, c0));
-        y1 = f2_fma(x1, s1, f2_mul(y1, c1));
-        x0 = rx0;
-        x1 = rx1;
-      }
 #pragma unroll
-      for (int h = 0; h < GP; ++h) {
-        const uint64_t t = f2_fma(q2[h][0], x0, f2_fma(q2[h][1], x1, f2_fma(q2[h][2], y0, f2_mul(q2[h][3], y1))));
-        float lo, hi;
-        f2_unpack(t, lo, hi);
-        val[n * GP + h] = lo + hi;
-      }
-    }
-    // reduce over the LPK lanes: each halving step hands half of the values to the partner lane
-    {
-      int cnt = NV;
-#pragma unroll
-      for (int mask = LPK / 2; mask > 0; mask >>= 1) {
-        if (cnt > 1) {
-          const bool up = ll & mask;
-#pragma unroll
-          for (int i = 0; i < NV / 2; ++i)
-            if (i < cnt / 2) {
-              const float send = up ? val[i] : val[i + cnt / 2], keep = up ? val[i + cnt / 2] : val[i];
-              val[i] = keep + __shfl_xor_sync(0xffffffffu, send, mask);
-            }
-          cnt >>= 1;
-        } else {
-          val[0] += __shfl_xor_sync(0xffffffffu, val[0], mask);
+        for (int h = 0; h < GP; ++h) {
+          const uint64_t t = f2_fma(q2[h][0], x0, f2_fma(q2[h][1], x1, f2_fma(q2[h][2], y0, f2_mul(q2[h][3], y1))));
+          float lo, hi;
+          f2_unpack(t, lo, hi);
+          val[n * GP + h] = lo + hi;
         }
       }
-    }
-    // this lane's own scores: key n = idx / GP, head idx % GP
-    bool grew = false;
-    float alpha[OWN];
+      // reduce over the LPK lanes: each halving step hands half of the values to the partner lane
+      {
+        int cnt = NV;
 #pragma unroll
-    for (int u = 0; u < OWN; ++u) {
-      const int n = (own0 + u) / GP, h = (own0 + u) % GP, slot = base + n * KPW + kg;
-      const bool near = __shfl_sync(0xffffffffu, static_cast<int>(is_local), n * KPW + kg);
-      if (slot >= s_end || (a.window && !near)) val[u] = -INFINITY;
-      if (a.scores && slot < s_end && h < g && first_copy)
-        a.scores[(static_cast<long long>(b) * a.hq + kvh * g + h) * a.pitch + slot] = val[u];
-      float mx = val[u];
+        for (int mask = LPK / 2; mask > 0; mask >>= 1) {
+          if (cnt > 1) {
+            const bool up = ll & mask;
 #pragma unroll
-      for (int mask = 1; mask < 32; mask <<= 1)
-        if (!head_bit(mask)) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, mask));
-      const float m_new = fmaxf(m_own[u], mx);
-      alpha[u] = m_new == -INFINITY ? 1.f : fast_exp2(m_own[u] - m_new);
-      grew |= m_new > m_own[u];
-      m_own[u] = m_new;
-      const float p = val[u] == -INFINITY ? 0.f : fast_exp2(val[u] - m_new);
-      l_own[u] = l_own[u] * alpha[u] + p;
-      if (first_copy) sp[warp][kg][own0 + u] = p;
-    }
-    if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-      for (int h = 0; h < GP; ++h) {
-        const float f = __shfl_sync(0xffffffffu, alpha[h % OWN], h * LPK / NV);
-        const uint64_t f2 = f2_pack(f, f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o2[h][e] = f2_mul(o2[h][e], f2);
+            for (int i = 0; i < NV / 2; ++i)
+              if (i < cnt / 2) {
+                const float send = up ? val[i] : val[i + cnt / 2], keep = up ? val[i + cnt / 2] : val[i];
+                val[i] = keep + __shfl_xor_sync(0xffffffffu, send, mask);
+              }
+            cnt >>= 1;
+          } else {
+            val[0] += __shfl_xor_sync(0xffffffffu, val[0], mask);
+          }
+        }
       }
-    }
-    __syncwarp();
+      // this lane's own scores: key n = idx / GP, head idx % GP
+      bool grew = false;
+      float alpha[OWN];
 #pragma unroll
-    for (int n = 0; n < NK; ++n) {
-      const uint64_t v0 = bf16x2_to_f2(v[n].x), v1 = bf16x2_to_f2(v[n].y), v2 = bf16x2_to_f2(v[n].z), v3 = bf16x2_to_f2(v[n].w);
+      for (int u = 0; u < OWN; ++u) {
+        const int n = (own0 + u) / GP, h = (own0 + u) % GP, slot = sbase + n * KPW + kg;
+        const bool near = (local_mask >> (sub * CH + n * KPW + kg)) & 1u;
+        if (slot >= s_end || (a.window && !near)) val[u] = -INFINITY;
+        if (score_at && slot < s_end && h < g && first_copy) score_at[static_cast<long long>(h) * a.pitch + slot] = val[u];
+        float mx = val[u];
 #pragma unroll
-      for (int h = 0; h < GP; ++h) {
-        const float p = sp[warp][kg][n * GP + h];
-        const uint64_t p2 = f2_pack(p, p);
-        o2[h][0] = f2_fma(p2, v0, o2[h][0]);
-        o2[h][1] = f2_fma(p2, v1, o2[h][1]);
-        o2[h][2] = f2_fma(p2, v2, o2[h][2]);
-        o2[h][3] = f2_fma(p2, v3, o2[h][3]);
+        for (int mask = 1; mask < 32; mask <<= 1)
+          if (!head_bit(mask)) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, mask));
+        const float m_new = fmaxf(m_own[u], mx);
+        alpha[u] = m_new == -INFINITY ? 1.f : fast_exp2(m_own[u] - m_new);
+        grew |= m_new > m_own[u];
+        m_own[u] = m_new;
+        const float p = val[u] == -INFINITY ? 0.f : fast_exp2(val[u] - m_new);
+        l_own[u] = l_own[u] * alpha[u] + p;
+        if (first_copy) sp[warp][kg][own0 + u] = make_float2(p, p);
       }
+      if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int h = 0; h < GP; ++h) {
+          const float f = __shfl_sync(0xffffffffu, alpha[h % OWN], h * LPK / NV);
+          const uint64_t f2 = f2_pack(f, f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o2[h][e] = f2_mul(o2[h][e], f2);
+        }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int n = 0; n < NK; ++n) {
+        const uint4 v = *reinterpret_cast<const uint4*>(st + (n * KPW + kg) * (D * 4) + 2 * D + ll * 16);
+        const uint64_t v0 = bf16x2_to_f2(v.x), v1 = bf16x2_to_f2(v.y), v2 = bf16x2_to_f2(v.z), v3 = bf16x2_to_f2(v.w);
+#pragma unroll
+        for (int h = 0; h < GP; ++h) {
+          const uint64_t p2 = *reinterpret_cast<const uint64_t*>(&sp[warp][kg][n * GP + h]);
+          o2[h][0] = f2_fma(p2, v0, o2[h][0]);
+          o2[h][1] = f2_fma(p2, v1, o2[h][1]);
+          o2[h][2] = f2_fma(p2, v2, o2[h][2]);
+          o2[h][3] = f2_fma(p2, v3, o2[h][3]);
+        }
+      }
+      __syncwarp();  // sp and the stage are free again
+      stage = stage == STAGES - 1 ? 0 : stage + 1;
     }
-    __syncwarp();  // sp is rewritten by the next chunk
+    row = nrow;
+    pos = npos;
+    lookup(base + 2 * WARPS * 32, nrow, npos);
   }
+  cp_async_wait<0>();
+  __syncthreads();  // every warp is done with its stages: the merge reuses them
+  float (*so)[GP][D] = reinterpret_cast<float(*)[GP][D]>(smem);
 
   // merge: lane groups by shuffles, warps through shared memory in a fixed order
 #pragma unroll
@@ -393,21 +434,23 @@ __global__ void __launch_bounds__(kept::WARPS * 32) decode_kept_kernel(const __g
 // the log-sum-exps of the head's group from the partial maxima and sums (a few hundred bytes); x = 0
 // writes out and lse, and each x the weights of its SLOTS slots.
 constexpr int KEPT_FINISH_THREADS = 256, KEPT_FINISH_SLOTS = 1024;
+constexpr int KEPT_FACTORS = 1024;  // (head, range) factors held in shared memory at a time
 
 template <int D>
 __global__ void __launch_bounds__(KEPT_FINISH_THREADS) decode_kept_finish_kernel(const __grid_constant__ KeptArgs a) {
   __shared__ float s_lse2[kept::MAX_G];
+  __shared__ float s_f[KEPT_FACTORS];
   pdl_launch_dependents();
   pdl_wait();
   const int kvh = blockIdx.y, b = blockIdx.z, g = a.hq / a.hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const KeptSeq seq = kept_seq(a, b);
+  const long long head0 = static_cast<long long>(b) * a.hq + kvh * g;
   if (!seq.ok) {
     if (blockIdx.x == 0)
       for (int i = threadIdx.x; i < g * D; i += KEPT_FINISH_THREADS) {
-        const long long h = static_cast<long long>(b) * a.hq + kvh * g + i / D;
-        a.out[h * D + i % D] = __float2bfloat16(__int_as_float(0x7fc00000));
-        if (a.lse && i % D == 0) a.lse[h] = __int_as_float(0x7fc00000);
+        a.out[head0 * D + i] = __float2bfloat16(__int_as_float(0x7fc00000));
+        if (a.lse && i % D == 0) a.lse[head0 + i / D] = __int_as_float(0x7fc00000);
       }
     return;
   }
@@ -415,11 +458,12 @@ __global__ void __launch_bounds__(KEPT_FINISH_THREADS) decode_kept_finish_kernel
   if (blockIdx.x > 0 && beg >= seq.n) return;
   const int n_split = (seq.n + a.split_len - 1) / a.split_len;
   if (warp < g) {
-    const float* ml = a.part_ml + (static_cast<long long>(b) * a.hq + kvh * g + warp) * a.n_split * 2;
+    const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + (head0 + warp) * a.n_split;
     float m = -INFINITY, l = 0.f;
     for (int i = lane; i < n_split; i += 32) {
-      const float mi = ml[2 * i], M = fmaxf(m, mi);
-      if (M > -INFINITY) l = l * fast_exp2(m - M) + ml[2 * i + 1] * fast_exp2(mi - M);
+      const float2 x = ml[i];
+      const float M = fmaxf(m, x.x);
+      if (M > -INFINITY) l = l * fast_exp2(m - M) + x.y * fast_exp2(x.x - M);
       m = M;
     }
 #pragma unroll
@@ -433,27 +477,80 @@ __global__ void __launch_bounds__(KEPT_FINISH_THREADS) decode_kept_finish_kernel
   }
   __syncthreads();
   if (blockIdx.x == 0) {
-    for (int i = threadIdx.x; i < g * D; i += KEPT_FINISH_THREADS) {
-      const int h = i / D, d = i % D;
-      const long long head = static_cast<long long>(b) * a.hq + kvh * g + h;
-      float acc = 0.f;
-      for (int sp = 0; sp < n_split; ++sp)
-        acc += a.part_o[(head * a.n_split + sp) * D + d] * fast_exp2(a.part_ml[(head * a.n_split + sp) * 2] - s_lse2[h]);
-      a.out[head * D + d] = __float2bfloat16(acc);
-      if (a.lse && d == 0) a.lse[head] = s_lse2[h] * 0.69314718055994530942f;
+    // out: four values a thread, the ranges dealt to the thread groups that share them
+    constexpr int Q = D / 4;                       // threads a head's row
+    const int rows_par = KEPT_FINISH_THREADS / Q;  // rows in flight, 8 at least: (head, slice of the ranges)
+    const int per = KEPT_FACTORS / kept::MAX_G;    // ranges a round
+    __shared__ float4 s_part[KEPT_FINISH_THREADS];
+    const int slices = max(1, rows_par / g);       // slices a head
+    const int rr = threadIdx.x / Q, d4 = threadIdx.x % Q;
+    const int h = rr % g, sl = rr / g;
+    const bool on = sl < slices && rr < g * slices;
+    {
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int r0 = 0; r0 < n_split; r0 += per) {
+        const int cnt = min(per, n_split - r0);
+        __syncthreads();
+        for (int i = threadIdx.x; i < g * cnt; i += KEPT_FINISH_THREADS) {
+          const int hh = i / cnt, sp = i % cnt;
+          s_f[hh * per + sp] = fast_exp2(a.part_ml[((head0 + hh) * a.n_split + r0 + sp) * 2] - s_lse2[hh]);
+        }
+        __syncthreads();
+        if (on) {
+          const float4* src = reinterpret_cast<const float4*>(a.part_o + ((head0 + h) * a.n_split + r0) * D) + d4;
+#pragma unroll 4
+          for (int sp = sl; sp < cnt; sp += slices) {
+            const float4 x = src[static_cast<long long>(sp) * Q];
+            const float f = s_f[h * per + sp];
+            acc.x += x.x * f;
+            acc.y += x.y * f;
+            acc.z += x.z * f;
+            acc.w += x.w * f;
+          }
+        }
+      }
+      s_part[threadIdx.x] = acc;
+      __syncthreads();
+      if (on && sl == 0) {
+        for (int i = 1; i < slices; ++i) {
+          const float4 x = s_part[(i * g + h) * Q + d4];
+          acc.x += x.x;
+          acc.y += x.y;
+          acc.z += x.z;
+          acc.w += x.w;
+        }
+        *reinterpret_cast<uint2*>(a.out + (head0 + h) * D + 4 * d4) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+        if (a.lse && d4 == 0) a.lse[head0 + h] = s_lse2[h] * 0.69314718055994530942f;
+      }
     }
   }
   if (!a.kweight) return;
+  // four slots a thread in flight
   const int end = min(seq.n, beg + KEPT_FINISH_SLOTS);
-  for (int slot = beg + threadIdx.x; slot < end; slot += KEPT_FINISH_THREADS) {
-    const long long r = cache_row(a.rows, b, slot, 0);
-    if (r < 0) continue;
-    float w = 0.f;
-    for (int h = 0; h < g; ++h)
-      w += fast_exp2(a.scores[(static_cast<long long>(b) * a.hq + kvh * g + h) * a.pitch + slot] - s_lse2[h]);
-    float* dst = a.kweight + static_cast<long long>(kvh) * a.rows.rows + r;
-    *dst = slot == seq.n - 1 ? w : *dst + w;  // the new token's slot starts at zero
+  const float* sc = a.scores + head0 * a.pitch;
+  constexpr int U = KEPT_FINISH_SLOTS / KEPT_FINISH_THREADS;
+  float w[U], old[U];
+  long long at[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int slot = beg + u * KEPT_FINISH_THREADS + threadIdx.x;
+    at[u] = -1;
+    w[u] = old[u] = 0.f;
+    if (slot < end) {
+      const long long r = cache_row(a.rows, b, slot, 0);
+      if (r >= 0) at[u] = static_cast<long long>(kvh) * a.rows.rows + r;
+    }
+    if (at[u] >= 0 && slot != seq.n - 1) old[u] = a.kweight[at[u]];  // the new token's slot starts at zero
   }
+  for (int h = 0; h < g; ++h)
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int slot = beg + u * KEPT_FINISH_THREADS + threadIdx.x;
+      if (slot < end) w[u] += fast_exp2(sc[static_cast<long long>(h) * a.pitch + slot] - s_lse2[h]);
+    }
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (at[u] >= 0) a.kweight[at[u]] = old[u] + w[u];
 }
 
 }  // namespace bf

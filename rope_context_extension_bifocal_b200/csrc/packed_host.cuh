@@ -266,14 +266,22 @@ bf_status_t check_kept(int32_t batch, int32_t max_len, const bf_params_t* p) {
   return BF_OK;
 }
 
+template <int D, int GP>
+cudaError_t launch_kept_g(const bf::KeptArgs& a, int batch, cudaStream_t st) {
+  constexpr int smem = bf::kept_smem_bytes<D, GP>();
+  auto kern = bf::decode_kept_kernel<D, GP>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(a.n_split, a.hkv, batch), dim3(bf::kept::WARPS * 32), smem, st, a);
+}
+
 template <int D>
 cudaError_t launch_kept(const bf::KeptArgs& a, int batch, cudaStream_t st) {
-  const dim3 grid(a.n_split, a.hkv, batch), block(bf::kept::WARPS * 32);
   const int g = a.hq / a.hkv;
-  cudaError_t e = g == 1   ? launch_pdl(bf::decode_kept_kernel<D, 1>, grid, block, 0, st, a)
-                  : g == 2 ? launch_pdl(bf::decode_kept_kernel<D, 2>, grid, block, 0, st, a)
-                  : g <= 4 ? launch_pdl(bf::decode_kept_kernel<D, 4>, grid, block, 0, st, a)
-                           : launch_pdl(bf::decode_kept_kernel<D, 8>, grid, block, 0, st, a);
+  const cudaError_t e = g == 1   ? launch_kept_g<D, 1>(a, batch, st)
+                        : g == 2 ? launch_kept_g<D, 2>(a, batch, st)
+                        : g <= 4 ? launch_kept_g<D, 4>(a, batch, st)
+                                 : launch_kept_g<D, 8>(a, batch, st);
   if (e != cudaSuccess) return e;
   const int64_t chunks = a.kweight ? (static_cast<int64_t>(a.max_len) + bf::KEPT_FINISH_SLOTS - 1) / bf::KEPT_FINISH_SLOTS : 1;
   return launch_pdl(bf::decode_kept_finish_kernel<D>, dim3(static_cast<unsigned>(chunks), a.hkv, batch),
@@ -301,6 +309,9 @@ bf_status_t decode_kept_impl(const void* q, const void* k_new, const void* v_new
   if (!workspace || !aligned(workspace, 256) || ws_bytes < lay.total) return BF_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const Rope rope = make_rope(p->rope_theta, p->head_dim, 1);
+  a.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (page_size == 1 << i) a.page_shift = i;
   a.q = static_cast<const bf16*>(q);
   a.k_new = static_cast<const bf16*>(k_new);
   a.v_new = static_cast<const bf16*>(v_new);
