@@ -11,9 +11,7 @@
 // so every key is turned by C(its position, or the query's when it is local): one form of the query,
 // no branch per key, and keys of both kinds may lie in any order. C(p) turns pair k by m(p) c_k,
 // with m = p, c_k = w_k (1/G - 1) under frequency interpolation and m = p - floor(p / G), c_k = -w_k
-// under position aliasing. c_k is held as a fraction of a turn, 32 bits of it as an integer and the
-// rest as a float: the integer product m c_k wraps at whole turns by itself, so the reduced angle
-// costs an integer multiplication and an FMA, exact to 2^-23 turns at any position.
+// under position aliasing (angles as in turn_cos_sin).
 //
 // What bounds it: 4 D bytes of K and V a slot and kv head from HBM, and, next to that, instructions
 // (about 50 a slot and kv head and warp for four query heads at D = 128: half of them the sines and
@@ -167,8 +165,7 @@ __global__ void __launch_bounds__(kept::WARPS * 32, GP <= 4 ? 4 : 2) decode_kept
   // the query heads' rows under R_l(now) (R_o when nothing is long-range), in the log2 domain, and
   // the turn fractions of the correction: this lane's pairs 4 ll .. 4 ll + 3
   uint64_t q2[GP][4];  // packed pairs: x of pairs (0,1), (2,3); y of pairs (0,1), (2,3)
-  uint32_t whi[4];
-  float wlo[4];
+  TurnStep corr[4];
   {
     float c[4], s[4];
 #pragma unroll
@@ -178,11 +175,7 @@ __global__ void __launch_bounds__(kept::WARPS * 32, GP <= 4 ? 4 : 2) decode_kept
                          : a.mode == 0 ? static_cast<double>(seq.now) * (w / seq.G)
                                        : static_cast<double>(seq.now / seq.G) * w;
       angle_cos_sin(ang, c[e], s[e]);
-      double t = (a.mode == 0 ? w / seq.G - w : -w) * 0.15915494309189533576888376337251;  // turns a unit of m
-      t = (t - floor(t)) * 4294967296.0;
-      const double hi = fmin(floor(t), 4294967295.0);
-      whi[e] = static_cast<uint32_t>(hi);
-      wlo[e] = static_cast<float>((t - hi) * (2.3283064365386962890625e-10 * 6.283185307179586476925286766559));
+      corr[e] = turn_step(a.mode == 0 ? w / seq.G - w : -w);
     }
 #pragma unroll
     for (int h = 0; h < GP; ++h) {
@@ -287,12 +280,7 @@ __global__ void __launch_bounds__(kept::WARPS * 32, GP <= 4 ? 4 : 2) decode_kept
           const float mf = static_cast<float>(m);
           float c[4], s[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            // the wrapped product's top bits as the mantissa of f in [1, 2): f - 1.5 turns, in [-1/2, 1/2)
-            const uint32_t ph = static_cast<uint32_t>(m) * whi[e] + 0x80000100u;
-            const float f = __uint_as_float(__funnelshift_r(ph, 0x7fu, 9));
-            __sincosf(fmaf(f, 6.283185307179586f, fmaf(mf, wlo[e], -9.42477796076938f)), &s[e], &c[e]);
-          }
+          for (int e = 0; e < 4; ++e) turn_cos_sin(m, mf, corr[e], c[e], s[e]);
           const uint64_t c0 = f2_pack(c[0], c[1]), c1 = f2_pack(c[2], c[3]), s0 = f2_pack(s[0], s[1]), s1 = f2_pack(s[2], s[3]);
           const uint64_t rx0 = f2_sub(f2_mul(x0, c0), f2_mul(y0, s0)), rx1 = f2_sub(f2_mul(x1, c1), f2_mul(y1, s1));
           y0 = f2_fma(x0, s0, f2_mul(y0, c0));

@@ -3,13 +3,17 @@
 // exp(score - lse_i), with the prefill's log-sum-exps.
 //
 // One CTA owns 128 keys of one kv head and streams the query tiles that see them: S^T = K Q^T, keys in
-// the 128 tensor-memory lanes and 128 queries in the columns. A thread so owns one key, and the column
+// the 128 tensor-memory lanes and QT queries in the columns. A thread so owns one key, and the column
 // sum of the attention matrix is a sum along its own registers: no shuffles, no atomics, and a result
-// that does not depend on the order in which CTAs run.
+// that does not depend on the order in which CTAs run. The rows of the query forms are (query, head of the
+// group) with the heads innermost, so a tile holds QT / g queries of all g heads: a window of 32 queries and
+// four heads is one tile of 128 columns, not four with 32 each.
 //
 // Precision. A single fp16 rounding of the rotated operands moves a score by about 3e-4, and so a weight
 // summed from few queries by as much, relative. Each operand is therefore split into an fp16 value and the
-// fp16 rest, and S = Kh Qh + Kl Qh + Kh Ql (the term left out is 2^-22): scores exact to about 1e-6.
+// fp16 rest, and S = Kh Qh + Kl Qh + Kh Ql (the term left out is 2^-22): scores exact to about 1e-6. The errors
+// of a sum of many terms average out as one over the root of their number, so from SINGLE_FROM (query,
+// head) rows on one product is enough: 3e-4 / 128 (a third of the tensor work and half the query bytes).
 //
 // Keys come raw from global memory and are turned by the softmax warps themselves, once for each branch
 // the tile has (the local queries first, then the long-range ones); no rotated copy of k is written. The
@@ -17,9 +21,15 @@
 //
 // Warp roles: warps 0..7 form the key tile and then sum (two groups of four warps, one visit each in
 // turn; warp w reads TMEM lanes 32 (w % 4) ..), warp 8 = TMA producer, warp 9 = MMA issuer. A visit is one
-// query tile of one head under one branch. Tensor memory holds four S tiles, shared memory the key tile
-// (high and low part) and a ring of four query tiles.
+// query tile under one branch. Tensor memory holds four S tiles, shared memory the key tile (high and low
+// part) and a ring of query tiles.
+//
+// Few rows (QT = 64): each key tile has a handful of visits and its time is the latency of forming it, so two
+// CTAs share an SM (96 KB and 256 tensor-memory columns each). Many rows (QT = 128): one CTA, four 32 KB query
+// slots; bound by the 16 ex2 a clock (1024 clocks a visit, the product 512).
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 #include "decode.cuh"
 #include "packed.cuh"
@@ -30,25 +40,29 @@ namespace bf {
 
 namespace kw {
 constexpr int NBUF = 4;   // S tiles in tensor memory, and log-sum-exp rows in shared memory
-constexpr int NSLOT = 4;  // query tiles in the ring (two visits: a high and a low part each)
 constexpr int NTHREADS = 320;
-constexpr uint32_t HALF = 16384;  // 128 rows of 64 fp16 values
+constexpr uint32_t HALF = 16384;    // 128 rows of 64 fp16 values
+constexpr int SINGLE_FROM = 16384;  // (query, head) rows from which a single fp16 product is enough
+template <int QT>
+constexpr int slots() { return QT == 64 ? 2 : 4; }  // query tiles in the ring
 }  // namespace kw
 
 struct WeightArgs {
-  CUtensorMap qo_hi, qo_lo, ql_hi, ql_lo;  // [hq][Wp][D] fp16 query forms, box (64, 128, 1), 128-byte swizzle
+  CUtensorMap qo_hi, qo_lo, ql_hi, ql_lo;  // [hkv][form_rows * g][D] fp16 query forms, box (64, QT, 1), 128-byte swizzle
   const void* q;
   const void* k;      // [T, hkv, D] raw
   const float* lse;   // [hq, T]
   const int* cu;
   const PlanHeader* head;
-  const int2* tiles;
-  const int* qoff;    // [batch + 1] first row of a sequence's queries in the forms
+  const PackedTile* tiles;
+  const int* qoff;    // [batch + 1] first query of a sequence in the forms
   int batch, total_rows, hq, hkv, max_tiles;
   int obs, w0, w_pretrained, mode, window;
+  int head_major;     // CTAs in the order of kv heads (their query forms share L2), or of work alone
   __half* forms[4];   // the forms above, as weights_query_kernel writes them: Qo high, low, Ql high, low
-  float* nl;          // [hq][nl_pitch] -lse * log2(e) of the queries in the forms
-  int form_rows, nl_pitch;
+  float* nl;          // [hkv][nl_pitch] -lse * log2(e) of the rows of the forms
+  int form_rows;      // queries of the forms (g rows each)
+  long long nl_pitch;
   float scale_log2;
   float* kweight;     // [hkv, rows]
   CacheRows rows;
@@ -69,19 +83,9 @@ __device__ __forceinline__ void split_f16(const float (&x)[8], uint4& hi, uint4&
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// The angles of pairs k0 .. k0 + 7 at position p: original, or long-range with factor G.
-__device__ __forceinline__ void angles8(const double* omega, int k0, int p, int G, int mode, bool lng, float (&c)[8],
-                                        float (&s)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const double w = omega[k0 + i];
-    angle_cos_sin(!lng ? static_cast<double>(p) * w
-                       : mode == 0 ? static_cast<double>(p) * (w / G) : static_cast<double>(p / G) * w,
-                  c[i], s[i]);
-  }
-}
-
-// Query forms of the rows that count: one warp per row of the forms, lanes as in rope_packed_kernel.
+// Query forms of the rows that count: a warp for a query and every gridDim.y-th four heads (8 lanes a head, 8
+// pairs a lane). Many rows take all heads in one warp, which then forms its angles once; few rows are spread
+// over more warps instead, since their time is latency.
 template <typename Tin, int D>
 __global__ void __launch_bounds__(256) weights_query_kernel(const __grid_constant__ WeightArgs a) {
   constexpr int P = D / 2;
@@ -91,61 +95,104 @@ __global__ void __launch_bounds__(256) weights_query_kernel(const __grid_constan
   pdl_wait();
   const int w = blockIdx.x * 8 + warp;
   if (!a.head->ok || w >= a.qoff[a.batch]) return;
-  int b = sequence_of(a.qoff, a.batch, w);
+  const int b = sequence_of(a.qoff, a.batch, w);
   if (b < 0) return;
   const int first = a.cu[b], n = a.cu[b + 1] - first, cnt = window_rows(n, a.obs);
   const int i = w - a.qoff[b];
   if (i >= cnt) return;  // padding up to a multiple of four
   const int p = n - cnt + i, r = first + p;
-  const int G = factor_of(n, a.w_pretrained);
+  const int G = factor_of(n, a.w_pretrained), g = a.hq / a.hkv;
   const bool lng = !a.window && has_long_pairs(n, G, a.w0);
-  for (int h = lane; h < a.hq; h += 32)
-    a.nl[static_cast<long long>(h) * a.nl_pitch + w] =
-        -a.lse[static_cast<long long>(h) * a.total_rows + r] * 1.44269504088896340736f;
   const int grp = lane >> 3, l8 = lane & 7;
   if (l8 >= LANES_PER_ROW) return;
   const int k0 = l8 * 8;
-  bool fin = true;
+  float c[2][8], s[2][8];
   for (int f = 0; f < (lng ? 2 : 1); ++f) {
-    float c[8], s[8];
-    angles8(a.omega, k0, p, G, a.mode, f == 1, c, s);
-    for (int h = grp; h < a.hq; h += 4) {
-      const Tin* src = static_cast<const Tin*>(a.q) + (static_cast<long long>(r) * a.hq + h) * D;
-      Vec8<Tin> x1, x2;
-      x1.load(src + k0);
-      x2.load(src + P + k0);
+    const int m = f == 1 && a.mode != 0 ? p / G : p;
+    const float mf = static_cast<float>(m);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const double om = a.omega[k0 + e];
+      turn_cos_sin(m, mf, turn_step(f == 1 && a.mode == 0 ? om / G : om), f ? c[1][e] : c[0][e], f ? s[1][e] : s[0][e]);
+    }
+  }
+  const bool low = static_cast<long long>(cnt) * g < kw::SINGLE_FROM;
+  bool fin = true;
+  for (int h = blockIdx.y * 4 + grp; h < a.hq; h += gridDim.y * 4) {
+    const int kvh = h / g;
+    const long long row = static_cast<long long>(w) * g + h % g;  // of this kv head's rows
+    if (l8 == 0)
+      a.nl[kvh * a.nl_pitch + row] = -a.lse[static_cast<long long>(h) * a.total_rows + r] * 1.44269504088896340736f;
+    const Tin* src = static_cast<const Tin*>(a.q) + (static_cast<long long>(r) * a.hq + h) * D;
+    Vec8<Tin> x1, x2;
+    x1.load(src + k0);
+    x2.load(src + P + k0);
+    const long long at = (static_cast<long long>(kvh) * a.form_rows * g + row) * D;
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      if (f == 1 && !lng) break;
       float y1[8], y2[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float u = x1.get(e), v = x2.get(e);
-        y1[e] = u * c[e] - v * s[e];
-        y2[e] = v * c[e] + u * s[e];
+        y1[e] = u * c[f][e] - v * s[f][e];
+        y2[e] = v * c[f][e] + u * s[f][e];
       }
-      const long long at = (static_cast<long long>(h) * a.form_rows + w) * D;
       uint4 hi, lo;
       split_f16(y1, hi, lo, fin);
       *reinterpret_cast<uint4*>(a.forms[2 * f] + at + k0) = hi;
-      *reinterpret_cast<uint4*>(a.forms[2 * f + 1] + at + k0) = lo;
+      if (low) *reinterpret_cast<uint4*>(a.forms[2 * f + 1] + at + k0) = lo;
       split_f16(y2, hi, lo, fin);
       *reinterpret_cast<uint4*>(a.forms[2 * f] + at + P + k0) = hi;
-      *reinterpret_cast<uint4*>(a.forms[2 * f + 1] + at + P + k0) = lo;
+      if (low) *reinterpret_cast<uint4*>(a.forms[2 * f + 1] + at + P + k0) = lo;
     }
   }
   if (!fin) report_status(kDevRange, 90);
 }
 
-template <typename Tin, int D>
-__global__ void __launch_bounds__(kw::NTHREADS, 1) key_weights_kernel(const __grid_constant__ WeightArgs a) {
+// 2^x of two values on the FMA pipe: x = n + f with n the nearest integer (Cody and Waite's reduction, the
+// rounding done by adding 1.5 2^23), a polynomial of degree 5 in f fitted by weighted least squares to 2^f on
+// [-1/2, 1/2] (relative error 2.4e-7 in fp32), and 2^n as an exponent. x is held in [-126, 128] (a NaN stays).
+__device__ __forceinline__ uint64_t exp2_fma2(uint64_t x2) {
+  float x0, x1;
+  f2_unpack(x2, x0, x1);
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;\n\tmin.NaN.f32 %0, %0, 0f43000000;" : "+f"(x0));
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;\n\tmin.NaN.f32 %0, %0, 0f43000000;" : "+f"(x1));
+  x2 = f2_pack(x0, x1);
+  const uint64_t magic = f2_pack(12582912.f, 12582912.f);
+  const uint64_t y = f2_add(x2, magic);
+  const uint64_t f = f2_sub(x2, f2_sub(y, magic));
+  uint64_t p = f2_pack(1.327647129073739e-3f, 1.327647129073739e-3f);
+  p = f2_fma(p, f, f2_pack(9.675540961325169e-3f, 9.675540961325169e-3f));
+  p = f2_fma(p, f, f2_pack(5.550713092088699e-2f, 5.550713092088699e-2f));
+  p = f2_fma(p, f, f2_pack(2.4022120237350464e-1f, 2.4022120237350464e-1f));
+  p = f2_fma(p, f, f2_pack(6.931469440460205e-1f, 6.931469440460205e-1f));
+  p = f2_fma(p, f, f2_pack(1.0000001192092896f, 1.0000001192092896f));
+  float y0, y1;
+  f2_unpack(y, y0, y1);
+  const uint64_t e = f2_pack(__uint_as_float((__float_as_uint(y0) << 23) + 0x3f800000u),
+                             __uint_as_float((__float_as_uint(y1) << 23) + 0x3f800000u));
+  return f2_mul(p, e);
+}
+
+template <typename Tin, int D, int QT>
+__global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_kernel(const __grid_constant__ WeightArgs a) {
   using namespace kw;
   using tc::fence_after;
   using tc::fence_before;
   using tc::mma_commit;
   constexpr int P = D / 2;
-  constexpr uint32_t TILE = D / 64 * HALF;  // one 128-row operand tile
-  constexpr int KS = D / 16;                // K-steps of a product
+  constexpr int NSLOT = slots<QT>();
+  constexpr uint32_t KTILE = D / 64 * HALF;      // the key operand: 128 rows
+  constexpr uint32_t QHALF = QT * 128;           // 64 dimensions of QT query rows
+  constexpr uint32_t QTILE = D / 64 * QHALF;
+  constexpr int KS = D / 16;                     // K-steps of a product
+  constexpr uint32_t NCOL = NBUF * QT;           // tensor-memory columns
+  constexpr uint32_t IDESC = (1u << 4) | (static_cast<uint32_t>(QT / 8) << 17) | (8u << 24);  // f16 x f16 -> f32, 128 x QT
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ __align__(16) float s_nl[NBUF][128];
+  __shared__ __align__(16) float s_nl[NBUF][QT];
   __shared__ float s_sum[128];
+  __shared__ TurnStep s_step[2][P];  // original and long-range form
   __shared__ uint64_t q_full[NSLOT], q_empty[NSLOT], s_full[NBUF], s_free[NBUF], nl_full[NBUF], k_ready, k_free, drain;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int s_abort;
@@ -153,28 +200,34 @@ __global__ void __launch_bounds__(kw::NTHREADS, 1) key_weights_kernel(const __gr
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
   pdl_wait();
-  const int kvh = static_cast<int>(blockIdx.x) / a.max_tiles, rank = static_cast<int>(blockIdx.x) % a.max_tiles;
+  const int idx = static_cast<int>(blockIdx.x);
+  const int kvh = a.head_major ? idx / a.max_tiles : idx % a.hkv, rank = a.head_major ? idx % a.max_tiles : idx / a.hkv;
+  const PackedTile tile = a.tiles[rank];
   if (rank >= a.head->n_tiles) return;
-  const int2 tile = a.tiles[rank];
   const int g = a.hq / a.hkv;
-  const int first = a.cu[tile.x], L = a.cu[tile.x + 1] - first;
+  const int L = tile.n;
   const int cnt = window_rows(L, a.obs), start = L - cnt;  // queries start .. L - 1
-  const int j0 = tile.y * 128;
+  const int j0 = tile.t * 128;
   const int G = factor_of(L, a.w_pretrained);
   const bool lng_pairs = !a.window && has_long_pairs(L, G, a.w0);
   const int w0 = (a.window || lng_pairs) ? a.w0 : kAllLocal;
-  const int qrow = a.qoff[tile.x];
-  // Query tile t holds queries start + 128 t .. + 127. Tiles [t_first, t_oe) have local pairs with these
-  // keys, tiles [t_lb, n_t) long-range ones; a tile in both is visited under either branch.
-  const int n_t = (cnt + 127) / 128;
-  const int t_first = j0 > start ? (j0 - start) / 128 : 0;
-  auto tiles_below = [&](long long x) { return static_cast<int>(min(static_cast<long long>(n_t), max(static_cast<long long>(t_first), x > 0 ? (x + 127) / 128 : 0))); };
-  const int t_oe = w0 > 0 ? tiles_below(static_cast<long long>(w0) + j0 + 127 - start) : t_first;
-  const int t_lb = lng_pairs ? tiles_below(static_cast<long long>(w0) + j0 - 127 - start) : n_t;
-  const int n_o = (t_oe - t_first) * g, n_l = (n_t - t_lb) * g, nv = n_o + n_l;
+  const int rows = cnt * g;              // (query, head) rows
+  const int qrow = tile.qoff * g;        // their first row in the forms
+  const bool split = rows < SINGLE_FROM;
+  const int fpv = split ? 2 : 1;         // ring fills a visit
+  // Query tile t holds rows QT t .. QT t + QT - 1: queries start + QT t / g .. start + (QT t + QT - 1) / g. Tiles
+  // [t_first, t_oe) have local pairs with these keys, tiles [t_lb, n_t) long-range ones; a tile in both is
+  // visited under either branch.
+  const int n_t = (rows + QT - 1) / QT;
+  const int t_first = j0 > start ? static_cast<int>(static_cast<long long>(j0 - start) * g / QT) : 0;
+  auto clamp_t = [&](long long x) { return static_cast<int>(min(static_cast<long long>(n_t), max(static_cast<long long>(t_first), x))); };
+  const long long x_loc = (static_cast<long long>(w0) + j0 + 127 - start) * g, x_far = (static_cast<long long>(w0) + j0 - start) * g;
+  const int t_oe = w0 > 0 ? clamp_t(x_loc > 0 ? (x_loc + QT - 1) / QT : 0) : t_first;
+  const int t_lb = lng_pairs ? clamp_t(x_far > 0 ? x_far / QT : 0) : n_t;
+  const int n_o = t_oe - t_first, n_l = n_t - t_lb, nv = n_o + n_l;
 
   const uint32_t base = smem_u32(smem);
-  const uint32_t k_hi = base, k_lo = base + TILE, ring = base + 2 * TILE;
+  const uint32_t k_hi = base, k_lo = base + KTILE, ring = base + 2 * KTILE;
   if (threadIdx.x == 0) {
     s_abort = 0;
     for (int i = 0; i < NSLOT; ++i) {
@@ -191,54 +244,51 @@ __global__ void __launch_bounds__(kw::NTHREADS, 1) key_weights_kernel(const __gr
     mbar_init(&drain, 1);
     fence_barrier_init();
   }
+  if (threadIdx.x < P) {
+    const double om = a.omega[threadIdx.x];
+    s_step[0][threadIdx.x] = turn_step(om);
+    s_step[1][threadIdx.x] = turn_step(a.mode == 0 ? om / G : om);
+  }
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_sh)),
-                 "r"(512));
+                 "r"(NCOL));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = tmem_base_sh;
-  // tile and head (within the group) of visit v
-  auto visit = [&](int v, int& t, int& hg, bool& lng) {
-    lng = v >= n_o;
-    const int u = lng ? v - n_o : v;
-    t = (lng ? t_lb : t_first) + u / g;
-    hg = u % g;
-  };
+  auto tile_of = [&](int v) { return v >= n_o ? t_lb + v - n_o : t_first + v; };
 
   if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       uint32_t used = 0, par = 0, nl_used = 0, nl_par = 0;
       for (int v = 0; v < nv; ++v) {
-        int t, hg;
-        bool lng;
-        visit(v, t, hg, lng);
-        const int h = kvh * g + hg, buf = v % NBUF;
+        const int t = tile_of(v), buf = v % NBUF;
+        const bool lng = v >= n_o;
         // the buffer's log-sum-exp row is free once its last visit has been summed
         if (v >= NBUF && !mbar_wait_abortable(&s_free[buf], (v / NBUF - 1) & 1, 100, &s_abort)) break;
-        mbar_arrive_expect_tx(&nl_full[buf], 512);
+        mbar_arrive_expect_tx(&nl_full[buf], QT * 4);
         asm volatile(
             "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
                 smem_u32(&s_nl[buf][0])),
-            "l"(a.nl + static_cast<long long>(h) * a.nl_pitch + qrow + t * 128), "r"(512), "r"(smem_u32(&nl_full[buf]))
+            "l"(a.nl + kvh * a.nl_pitch + qrow + t * QT), "r"(QT * 4), "r"(smem_u32(&nl_full[buf]))
             : "memory");
         nl_used |= 1u << buf;
         nl_par ^= 1u << buf;
         bool ok = true;
-        for (int x = 0; x < 2 && ok; ++x) {
-          const int n = 2 * v + x, slot = n % NSLOT;
+        for (int x = 0; x < fpv; ++x) {
+          const int n = fpv * v + x, slot = n % NSLOT;
           if (n >= NSLOT && !mbar_wait_abortable(&q_empty[slot], (n / NSLOT - 1) & 1, 101, &s_abort)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&q_full[slot], TILE);
+          mbar_arrive_expect_tx(&q_full[slot], QTILE);
           const CUtensorMap* m = lng ? (x == 0 ? &a.ql_hi : &a.ql_lo) : (x == 0 ? &a.qo_hi : &a.qo_lo);
 #pragma unroll
           for (int hf = 0; hf < D / 64; ++hf)
-            tma_load_3d(smem + (ring - base) + slot * TILE + hf * HALF, m, &q_full[slot], 64 * hf, qrow + t * 128, h);
+            tma_load_3d(smem + (ring - base) + slot * QTILE + hf * QHALF, m, &q_full[slot], 64 * hf, qrow + t * QT, kvh);
           used |= 1u << slot;
           par ^= 1u << slot;
         }
@@ -256,27 +306,30 @@ __global__ void __launch_bounds__(kw::NTHREADS, 1) key_weights_kernel(const __gr
       const uint64_t dkh = tc::k_desc(k_hi, 0), dkl = tc::k_desc(k_lo, 0), dq0 = tc::k_desc(ring, 0);
       auto product = [&](uint32_t d, uint64_t da, uint64_t db, bool acc) {
 #pragma unroll
-        for (int kk = 0; kk < KS; ++kk) {
-          const uint64_t step = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
-          tc2::mma_ss(d, da + step, db + step, tc::IDESC_QK, acc || kk > 0);
-        }
+        for (int kk = 0; kk < KS; ++kk)
+          tc2::mma_ss(d, da + (((kk >> 2) * HALF + (kk & 3) * 32) >> 4), db + (((kk >> 2) * QHALF + (kk & 3) * 32) >> 4),
+                      IDESC, acc || kk > 0);
       };
       for (int v = 0; v < nv; ++v) {
-        const int buf = v % NBUF, hi = (2 * v) % NSLOT, lo = (2 * v + 1) % NSLOT;
+        const int buf = v % NBUF, n0 = fpv * v, hi = n0 % NSLOT, lo = (n0 + 1) % NSLOT;
         if (v == 0 && !mbar_wait_abortable(&k_ready, 0, 110, &s_abort)) break;
         if (v == n_o && n_o > 0 && !mbar_wait_abortable(&k_ready, 1, 111, &s_abort)) break;
         if (v >= NBUF && !mbar_wait_abortable(&s_free[buf], (v / NBUF - 1) & 1, 112, &s_abort)) break;
-        if (!mbar_wait_abortable(&q_full[hi], ((2 * v) / NSLOT) & 1, 113, &s_abort)) break;
+        if (!mbar_wait_abortable(&q_full[hi], (n0 / NSLOT) & 1, 113, &s_abort)) break;
         fence_after();
-        const uint32_t d = tmem + buf * 128;
-        const uint64_t bh = dq0 + static_cast<uint64_t>(hi * (TILE >> 4)), bl = dq0 + static_cast<uint64_t>(lo * (TILE >> 4));
+        const uint32_t d = tmem + buf * QT;
+        const uint64_t bh = dq0 + static_cast<uint64_t>(hi * (QTILE >> 4)), bl = dq0 + static_cast<uint64_t>(lo * (QTILE >> 4));
         product(d, dkh, bh, false);
-        product(d, dkl, bh, true);
-        mma_commit(&q_empty[hi]);
-        if (!mbar_wait_abortable(&q_full[lo], ((2 * v + 1) / NSLOT) & 1, 114, &s_abort)) break;
-        fence_after();
-        product(d, dkh, bl, true);
-        mma_commit(&q_empty[lo]);
+        if (split) {
+          product(d, dkl, bh, true);
+          mma_commit(&q_empty[hi]);
+          if (!mbar_wait_abortable(&q_full[lo], ((n0 + 1) / NSLOT) & 1, 114, &s_abort)) break;
+          fence_after();
+          product(d, dkh, bl, true);
+          mma_commit(&q_empty[lo]);
+        } else {
+          mma_commit(&q_empty[hi]);
+        }
         mma_commit(&s_full[buf]);
         if (v == n_o - 1 && n_l > 0) mma_commit(&k_free);
       }
@@ -287,41 +340,52 @@ __global__ void __launch_bounds__(kw::NTHREADS, 1) key_weights_kernel(const __gr
     // ------------------------------------------------------------ key tile, then sums
     const int group = warp >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;
-    // The key tile under one branch, split in two: thread item = (row, 8 pairs); rows past the sequence are zero.
+    // The key tile under one branch, split in two: a thread has 8 pairs of every (256 / CPR)-th row; rows past the
+    // sequence are zero. The loads of RB rows are in flight together.
     auto form_keys = [&](bool lng) {
       bool fin = true;
-      constexpr int CPR = P / 8;  // items a row
+      constexpr int CPR = P / 8;               // threads a row
+      constexpr int RPT = 128 * CPR / 256;     // rows a thread
+      constexpr int RB = sizeof(Tin) == 2 ? RPT : RPT / 2;
+      const int c8 = threadIdx.x % CPR, k0 = c8 * 8, d2 = P + k0, row0 = threadIdx.x / CPR;
+      TurnStep step[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) step[e] = s_step[lng ? 1 : 0][k0 + e];
 #pragma unroll 1
-      for (int it = threadIdx.x; it < 128 * CPR; it += 256) {
-        const int row = it / CPR, c8 = it % CPR, k0 = c8 * 8;
-        float y1[8], y2[8];
-        if (j0 + row < L) {
-          const Tin* src = static_cast<const Tin*>(a.k) + (static_cast<long long>(first + j0 + row) * a.hkv + kvh) * D;
-          Vec8<Tin> x1, x2;
-          x1.load(src + k0);
-          x2.load(src + P + k0);
-          float c[8], s[8];
-          angles8(a.omega, k0, j0 + row, G, a.mode, lng, c, s);
+      for (int i0 = 0; i0 < RPT; i0 += RB) {
+        Vec8<Tin> x1[RB], x2[RB];
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+          const int row = row0 + (i0 + i) * (256 / CPR);
+          const Tin* src = static_cast<const Tin*>(a.k) +
+                           (static_cast<long long>(tile.first + min(j0 + row, L - 1)) * a.hkv + kvh) * D;
+          x1[i].load(src + k0);
+          x2[i].load(src + P + k0);
+        }
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+          const int row = row0 + (i0 + i) * (256 / CPR), j = j0 + row;
+          const int m = lng && a.mode != 0 ? j / G : j;
+          const float mf = static_cast<float>(m), in = j < L ? 1.f : 0.f;
+          float y1[8], y2[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float u = x1.get(e), v = x2.get(e);
-            y1[e] = u * c[e] - v * s[e];
-            y2[e] = v * c[e] + u * s[e];
+            float c, s;
+            turn_cos_sin(m, mf, step[e], c, s);
+            const float u = x1[i].get(e), v = x2[i].get(e);
+            y1[e] = in != 0.f ? u * c - v * s : 0.f;
+            y2[e] = in != 0.f ? v * c + u * s : 0.f;
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y1[e] = y2[e] = 0.f;
+          // element d of a row: half d / 64, 16-byte chunk (d % 64) / 8 of its 128 bytes, swizzled
+          const uint32_t o1 = (k0 / 64) * HALF + sw128(row, (k0 % 64) / 8), o2 = (d2 / 64) * HALF + sw128(row, (d2 % 64) / 8);
+          uint4 hi, lo;
+          split_f16(y1, hi, lo, fin);
+          *reinterpret_cast<uint4*>(smem + o1) = hi;
+          if (split) *reinterpret_cast<uint4*>(smem + KTILE + o1) = lo;
+          split_f16(y2, hi, lo, fin);
+          *reinterpret_cast<uint4*>(smem + o2) = hi;
+          if (split) *reinterpret_cast<uint4*>(smem + KTILE + o2) = lo;
         }
-        // element d of a row: half d / 64, 16-byte chunk (d % 64) / 8 of its 128 bytes, swizzled
-        const int d2 = P + k0;
-        const uint32_t o1 = (k0 / 64) * HALF + sw128(row, (k0 % 64) / 8), o2 = (d2 / 64) * HALF + sw128(row, (d2 % 64) / 8);
-        uint4 hi, lo;
-        split_f16(y1, hi, lo, fin);
-        *reinterpret_cast<uint4*>(smem + o1) = hi;
-        *reinterpret_cast<uint4*>(smem + TILE + o1) = lo;
-        split_f16(y2, hi, lo, fin);
-        *reinterpret_cast<uint4*>(smem + o2) = hi;
-        *reinterpret_cast<uint4*>(smem + TILE + o2) = lo;
       }
       if (!fin) report_status(kDevRange, 91);
       fence_proxy_async_smem();
@@ -343,56 +407,81 @@ __global__ void __launch_bounds__(kw::NTHREADS, 1) key_weights_kernel(const __gr
     for (int v = group; v < nv && ok; v += 2) {
       if (v >= n_o && !switched) to_long();
       if (!ok) break;
-      int t, hg;
-      bool lng;
-      visit(v, t, hg, lng);
-      const int buf = v % NBUF;
+      const int t = tile_of(v), buf = v % NBUF;
+      const bool lng = v >= n_o;
       if (!__all_sync(0xffffffffu, mbar_wait_abortable(&nl_full[buf], (v / NBUF) & 1, 121, &s_abort) &&
                                        mbar_wait_abortable(&s_full[buf], (v / NBUF) & 1, 122, &s_abort))) {
         ok = false;
         break;
       }
       fence_after();
-      const int i0 = start + t * 128;
-      const int dmin = i0 - (j0 + 127), dmax = i0 + 127 - j0;
-      const int valid = min(128, cnt - t * 128);
-      const bool masked = dmin < 0 || valid < 128 || (lng ? dmin < w0 : dmax >= w0);
-      const int lo = lng ? max(w0, 0) : 0, hi = lng ? 0x7fffffff : w0;
-      const int d0 = i0 - j0 - r;  // i - j of column 0
-      float part[4] = {0.f, 0.f, 0.f, 0.f};
+      const int r0 = t * QT, i0 = start + r0 / g, i1 = start + (r0 + QT - 1) / g;  // first and last query
+      const int dmin = i0 - (j0 + 127), dmax = i1 - j0;
+      const int valid = min(QT, rows - r0);
+      const uint32_t s_addr = lane_addr + buf * QT;
+      // Column c holds query i0 + (rem + c) / g; its distance i - j grows with c, so the columns that count are one
+      // range [c_lo, c_hi): (rem + c) / g >= x is c >= x g - rem.
+      int c_lo = 0, c_hi = QT;
+      const bool whole = dmin >= 0 && valid == QT && (lng ? dmin >= w0 : dmax < w0);
+      if (!whole) {
+        const int d0 = i0 - j0 - r, rem = r0 % g;
+        const long long lo = (static_cast<long long>(lng ? w0 : 0) - d0) * g - rem;
+        const long long hi = (static_cast<long long>(w0) - d0) * g - rem;
+        c_lo = static_cast<int>(min(max(lo, 0LL), static_cast<long long>(QT)));
+        c_hi = lng ? valid : static_cast<int>(min(max(hi, 0LL), static_cast<long long>(valid)));
+      }
+      auto add_up = [&](auto masked) {
+        const uint64_t sc2 = f2_pack(sc, sc);
+        const uint32_t span = c_hi > c_lo ? c_hi - c_lo : 0;
+        uint64_t acc[4];
 #pragma unroll
-      for (int c0 = 0; c0 < 128; c0 += 32) {
-        float s[32];
-        tc::tmem_ld32(lane_addr + buf * 128 + c0, s);
-        tc::wait_ld();
-        const float4* nl4 = reinterpret_cast<const float4*>(&s_nl[buf][c0]);
+        for (int u = 0; u < 4; ++u) acc[u] = f2_pack(0.f, 0.f);
+        float s[2][32];
+        tc::tmem_ld32(s_addr, s[0]);
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 nl = nl4[c / 4];
-          float p[4] = {fast_exp2(fmaf(s[c], sc, nl.x)), fast_exp2(fmaf(s[c + 1], sc, nl.y)),
-                        fast_exp2(fmaf(s[c + 2], sc, nl.z)), fast_exp2(fmaf(s[c + 3], sc, nl.w))};
-          if (masked) {
+        for (int c0 = 0; c0 < QT; c0 += 32) {
+          tc::wait_ld32(s[(c0 / 32) & 1]);
+          if (c0 + 32 < QT) tc::tmem_ld32(s_addr + c0 + 32, s[(c0 / 32 + 1) & 1]);
+          const float* x = s[(c0 / 32) & 1];
+          const ulonglong2* nl2 = reinterpret_cast<const ulonglong2*>(&s_nl[buf][c0]);
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const ulonglong2 nl = nl2[c / 4];
+            float p[4];
+            f2_unpack(f2_fma(f2_pack(x[c], x[c + 1]), sc2, nl.x), p[0], p[1]);
+            const uint64_t x23 = f2_fma(f2_pack(x[c + 2], x[c + 3]), sc2, nl.y);
+            if (!decltype(masked)::value && c % 8 == 4) {
+              // a quarter of the powers on the FMA pipe: the ex2 unit is what the loop waits for
+              acc[(c / 2) & 3] = f2_add(acc[(c / 2) & 3], f2_pack(fast_exp2(p[0]), fast_exp2(p[1])));
+              acc[(c / 2 + 1) & 3] = f2_add(acc[(c / 2 + 1) & 3], exp2_fma2(x23));
+              continue;
+            }
+            f2_unpack(x23, p[2], p[3]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int cc = c0 + c + e, d = d0 + cc;
-              p[e] = (cc < valid && d >= lo && d < hi) ? p[e] : 0.f;
+              p[e] = fast_exp2(p[e]);
+              if (decltype(masked)::value) p[e] = static_cast<uint32_t>(c0 + c + e - c_lo) < span ? p[e] : 0.f;
             }
+            acc[(c / 2) & 3] = f2_add(acc[(c / 2) & 3], f2_pack(p[0], p[1]));
+            acc[(c / 2 + 1) & 3] = f2_add(acc[(c / 2 + 1) & 3], f2_pack(p[2], p[3]));
           }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) part[e] += p[e];
         }
-      }
+        float lo, hi;
+        f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), lo, hi);
+        return lo + hi;
+      };
+      const float part = whole ? add_up(std::false_type()) : add_up(std::true_type());
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_free[buf]);
-      sum += (part[0] + part[1]) + (part[2] + part[3]);
+      sum += part;
     }
     if (!switched && ok) to_long();
     // the two groups' sums, in a fixed order
     if (group == 1) s_sum[r] = sum;
     asm volatile("bar.sync 1, 256;" ::: "memory");
     if (group == 0 && j0 + r < L && !*reinterpret_cast<volatile int*>(&s_abort)) {
-      const long long at = cache_row(a.rows, tile.x, j0 + r, first + j0 + r);
+      const long long at = cache_row(a.rows, tile.seq, j0 + r, tile.first + j0 + r);
       if (at < 0)
         report_status(kDevIndex, 92);
       else
@@ -402,12 +491,12 @@ __global__ void __launch_bounds__(kw::NTHREADS, 1) key_weights_kernel(const __gr
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(NCOL));
 }
 
-template <int D>
+template <int D, int QT>
 constexpr int key_weights_smem_bytes() {
-  return (2 + kw::NSLOT) * (D / 64) * static_cast<int>(kw::HALF);
+  return (D / 64) * (2 * static_cast<int>(kw::HALF) + kw::slots<QT>() * QT * 128);
 }
 
 }  // namespace bf

@@ -31,6 +31,12 @@ struct PlanHeader {
   int ok;
 };
 
+// One 128-row tile of a sequence: its index t within the sequence, the sequence's first row and its
+// length, and (key tiles) the first row of its queries in the query forms. All a CTA needs, in one load.
+struct __align__(32) PackedTile {
+  int seq, t, first, n, qoff, pad[3];
+};
+
 constexpr int kPlanLevels = 1024;
 
 struct PlanArgs {
@@ -38,7 +44,7 @@ struct PlanArgs {
   int batch, total_rows, max_len;
   int obs;        // key tiles: only the last `obs` rows of a sequence are queries; 0: query tiles
   PlanHeader* head;
-  int2* tiles;    // {sequence, tile within it}
+  PackedTile* tiles;
   int max_tiles;
   int* qoff;      // key tiles: [batch + 1] first row of each sequence's queries in the query forms
 };
@@ -115,16 +121,8 @@ __global__ void __launch_bounds__(1024) packed_plan_kernel(const __grid_constant
     }
   }
   __syncthreads();
-  for (int b = warp; b < a.batch; b += 32) {
-    const int n = a.cu[b + 1] - a.cu[b];
-    for (int t = lane; t * 128LL < n; t += 32) {
-      const int at = atomicAdd(&hist[level(n, t)], 1);
-      if (at < a.max_tiles) a.tiles[at] = make_int2(b, t);
-    }
-  }
-  if (!a.qoff) return;
   // exclusive scan of the sequences' query rows
-  for (int b0 = 0; b0 < a.batch; b0 += 1024) {
+  for (int b0 = 0; a.qoff && b0 < a.batch; b0 += 1024) {
     const int b = b0 + tid;
     const int c = b < a.batch ? window_pad(a.cu[b + 1] - a.cu[b], a.obs) : 0;
     int x = c;
@@ -143,7 +141,21 @@ __global__ void __launch_bounds__(1024) packed_plan_kernel(const __grid_constant
     if (tid == 1023) carry = before + x;
     __syncthreads();
   }
-  if (tid == 0) a.qoff[a.batch] = carry;
+  if (a.qoff && tid == 0) a.qoff[a.batch] = carry;
+  __syncthreads();  // the offsets are written: each warp reads those of its sequences
+  for (int b = warp; b < a.batch; b += 32) {
+    PackedTile e;
+    e.seq = b;
+    e.first = a.cu[b];
+    e.n = a.cu[b + 1] - e.first;
+    e.qoff = a.qoff ? a.qoff[b] : 0;
+    e.pad[0] = e.pad[1] = e.pad[2] = 0;
+    for (int t = lane; t * 128LL < e.n; t += 32) {
+      e.t = t;
+      const int at = atomicAdd(&hist[level(e.n, t)], 1);
+      if (at < a.max_tiles) a.tiles[at] = e;
+    }
+  }
 }
 
 // The sequence that packed row r belongs to (the last one that starts at or before r), or -1.
@@ -166,6 +178,31 @@ __device__ __forceinline__ int factor_of(int n, int w_pretrained) {
 
 // Whether a sequence of n rows has pairs in the long-range branch that differ from the original one.
 __device__ __forceinline__ bool has_long_pairs(int n, int G, int w0) { return G > 1 && w0 < n; }
+
+// Angles m * w for integers m, as fractions of a turn: `hi` is the first 32 bits of w / 2 pi, `lo` the rest
+// times 2 pi. The integer product m * hi wraps at whole turns by itself; its top 23 bits become the
+// mantissa of a float f in [1, 2), and (f - 1.5) turns, in [-1/2, 1/2), is the reduced angle: exact to 2^-23
+// turns (7e-7) at any m below 2^31, for an integer multiplication, a shift and two FMAs.
+struct TurnStep {
+  uint32_t hi;
+  float lo;
+};
+
+__device__ __forceinline__ TurnStep turn_step(double w) {
+  double t = w * 0.15915494309189533576888376337251;
+  t = (t - floor(t)) * 4294967296.0;
+  const double hi = fmin(floor(t), 4294967295.0);
+  TurnStep r;
+  r.hi = static_cast<uint32_t>(hi);
+  r.lo = static_cast<float>((t - hi) * (2.3283064365386962890625e-10 * 6.283185307179586476925286766559));
+  return r;
+}
+
+__device__ __forceinline__ void turn_cos_sin(int m, float mf, const TurnStep& w, float& c, float& s) {
+  const uint32_t ph = static_cast<uint32_t>(m) * w.hi + 0x80000100u;
+  const float f = __uint_as_float(__funnelshift_r(ph, 0x7fu, 9));
+  __sincosf(fmaf(f, 6.283185307179586f, fmaf(mf, w.lo, -9.42477796076938f)), &s, &c);
+}
 
 struct PackedRopeArgs {
   const void* q;
@@ -289,11 +326,10 @@ __global__ void __launch_bounds__(256) rope_packed_kernel(const __grid_constant_
 }
 
 // What the attention kernels' packed form adds to their arguments: the tile list and boundaries.
-// A CTA's tile is tiles[rank]; its sequence's rows start at cu[seq] and number cu[seq + 1] - cu[seq].
+// A CTA's tile is tiles[rank], if the list is that long.
 struct PackedTiles {
   const PlanHeader* head;
-  const int2* tiles;
-  const int* cu;
+  const PackedTile* tiles;
   int max_tiles;
   int total_rows;
   int w_pretrained;

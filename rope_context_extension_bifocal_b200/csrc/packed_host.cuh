@@ -35,7 +35,7 @@ bf_status_t check_packed(int32_t dtype, int32_t batch, int32_t total_rows, int32
 }
 
 cudaError_t launch_plan(const int32_t* cu, int batch, int total_rows, int max_len, int obs, bf::PlanHeader* head,
-                        int2* tiles, int max_tiles, int* qoff, cudaStream_t st) {
+                        bf::PackedTile* tiles, int max_tiles, int* qoff, cudaStream_t st) {
   bf::PlanArgs a{};
   a.cu = cu;
   a.batch = batch;
@@ -61,7 +61,7 @@ PackedLayout packed_layout(int dtype, int batch, int T, const bf_params_t* p) {
   const size_t qbytes = align256(static_cast<size_t>(T) * p->hq * p->head_dim * 2);
   const size_t kbytes = align256(static_cast<size_t>(T) * p->hkv * p->head_dim * 2);
   w.tiles = 256;
-  w.qo = w.tiles + align256(static_cast<size_t>(w.max_tiles) * sizeof(int2));
+  w.qo = w.tiles + align256(static_cast<size_t>(w.max_tiles) * sizeof(bf::PackedTile));
   w.ql = w.qo + qbytes;
   w.ko = w.ql + qbytes;
   w.kl = w.ko + kbytes;
@@ -113,7 +113,7 @@ bf_status_t prefill_packed_impl(const void* q, const void* k, const void* v, int
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const int D = p->head_dim;
   auto* head = reinterpret_cast<bf::PlanHeader*>(ws);
-  auto* tiles = reinterpret_cast<int2*>(ws + lay.tiles);
+  auto* tiles = reinterpret_cast<bf::PackedTile*>(ws + lay.tiles);
 
   // 1. the tile list
   if (launch_plan(cu_seqlens, batch, total_rows, max_len, 0, head, tiles, max_tiles, nullptr, st) != cudaSuccess)
@@ -162,7 +162,6 @@ bf_status_t prefill_packed_impl(const void* q, const void* k, const void* v, int
   bf::PackedTiles pt{};
   pt.head = head;
   pt.tiles = tiles;
-  pt.cu = cu_seqlens;
   pt.max_tiles = max_tiles;
   pt.total_rows = total_rows;
   pt.w_pretrained = p->w_pretrained;
@@ -461,37 +460,44 @@ WeightLayout weight_layout(int batch, int T, int obs, const bf_params_t* p) {
   w.rows = std::min<int64_t>(static_cast<int64_t>(T) + 3LL * batch, (static_cast<int64_t>(obs) + 3) * batch);
   w.rows = (w.rows + 3) / 4 * 4;
   w.tiles = 256;
-  w.qoff = w.tiles + align256(static_cast<size_t>(w.max_tiles) * sizeof(int2));
+  w.qoff = w.tiles + align256(static_cast<size_t>(w.max_tiles) * sizeof(bf::PackedTile));
   w.forms = w.qoff + align256((static_cast<size_t>(batch) + 1) * 4);
   w.form_bytes = align256(static_cast<size_t>(w.rows) * p->hq * p->head_dim * 2);
   w.nl = w.forms + 4 * w.form_bytes;
-  w.total = w.nl + align256((static_cast<size_t>(w.rows) + 128) * p->hq * 4);
+  w.total = w.nl + align256((static_cast<size_t>(w.rows) * (p->hq / p->hkv) + 128) * p->hkv * 4);
   return w;
 }
 
-// Operand forms [heads][rows][D] fp16, box (64, 128, 1), 128B swizzle.
-bool make_form_map(CUtensorMap* map, const void* base, int64_t rows, int heads, int D) {
+// Query forms [kv heads][rows][D] fp16, box (64, box_rows, 1), 128B swizzle.
+bool make_form_map(CUtensorMap* map, const void* base, int64_t rows, int heads, int D, int box_rows) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(heads)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(rows) * D * 2};
-  cuuint32_t box[3] = {64, 128, 1};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename Tin, int D>
-cudaError_t launch_weights(const bf::WeightArgs& a, cudaStream_t st) {
-  cudaError_t e = launch_pdl(bf::weights_query_kernel<Tin, D>, dim3(static_cast<unsigned>((a.form_rows + 7LL) / 8)),
-                             dim3(256), 0, st, a);
-  if (e != cudaSuccess) return e;
-  constexpr int smem = bf::key_weights_smem_bytes<D>();
-  auto kern = bf::key_weights_kernel<Tin, D>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <typename Tin, int D, int QT>
+cudaError_t launch_weights_qt(const bf::WeightArgs& a, cudaStream_t st) {
+  constexpr int smem = bf::key_weights_smem_bytes<D, QT>();
+  auto kern = bf::key_weights_kernel<Tin, D, QT>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(static_cast<unsigned>(a.max_tiles) * a.hkv), dim3(bf::kw::NTHREADS), smem, st, a);
+}
+
+template <typename Tin, int D>
+cudaError_t launch_weights(const bf::WeightArgs& a, int qt, cudaStream_t st) {
+  // all heads in one warp from 4096 queries on (512 CTAs)
+  const int y = a.form_rows >= 4096 ? 1 : (a.hq + 3) / 4;
+  const cudaError_t e = launch_pdl(bf::weights_query_kernel<Tin, D>,
+                                   dim3(static_cast<unsigned>((a.form_rows + 7LL) / 8), y), dim3(256), 0, st, a);
+  if (e != cudaSuccess) return e;
+  return qt == 64 ? launch_weights_qt<Tin, D, 64>(a, st) : launch_weights_qt<Tin, D, 128>(a, st);
 }
 
 bf_status_t key_weights_impl(const void* q, const void* k, int32_t dtype, const float* lse, int32_t total_rows,
@@ -515,17 +521,21 @@ bf_status_t key_weights_impl(const void* q, const void* k, int32_t dtype, const 
   obs = std::min(obs, max_len);
   const WeightLayout lay = weight_layout(batch, total_rows, obs, p);
   if (!workspace || !aligned(workspace, 256) || ws_bytes < lay.total) return BF_ERR_WORKSPACE;
-  if (lay.max_tiles * p->hkv > 0x7fffffffLL || lay.rows > 0x7ffffeffLL) return BF_ERR_UNSUPPORTED;
+  const int g = p->hq / p->hkv;
+  if (lay.max_tiles * p->hkv > 0x7fffffffLL || lay.rows * g > 0x7ffffe00LL || p->hq > 65535)
+    return BF_ERR_UNSUPPORTED;
+  // few rows a key tile: 64-row query tiles, two CTAs an SM
+  const int qt = static_cast<int64_t>(obs) * g <= 512 ? 64 : 128;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int D = p->head_dim;
   auto* head = reinterpret_cast<bf::PlanHeader*>(ws);
-  auto* tiles = reinterpret_cast<int2*>(ws + lay.tiles);
+  auto* tiles = reinterpret_cast<bf::PackedTile*>(ws + lay.tiles);
   int* qoff = reinterpret_cast<int*>(ws + lay.qoff);
   CUtensorMap* maps[4] = {&a.qo_hi, &a.qo_lo, &a.ql_hi, &a.ql_lo};
   for (int i = 0; i < 4; ++i) {
     a.forms[i] = reinterpret_cast<__half*>(ws + lay.forms + i * lay.form_bytes);
-    if (!make_form_map(maps[i], a.forms[i], lay.rows, p->hq, D)) return BF_ERR_CUDA;
+    if (!make_form_map(maps[i], a.forms[i], lay.rows * g, p->hkv, D, qt)) return BF_ERR_CUDA;
   }
   if (launch_plan(cu_seqlens, batch, total_rows, max_len, obs, head, tiles, static_cast<int>(lay.max_tiles), qoff, st) !=
       cudaSuccess)
@@ -550,15 +560,17 @@ bf_status_t key_weights_impl(const void* q, const void* k, int32_t dtype, const 
   a.window = (p->flags & BF_FLAG_WINDOW) ? 1 : 0;
   a.nl = reinterpret_cast<float*>(ws + lay.nl);
   a.form_rows = static_cast<int>(lay.rows);
-  a.nl_pitch = static_cast<int>(lay.rows) + 128;
+  a.nl_pitch = lay.rows * g + 128;
   a.scale_log2 = scale_log2(p);
+  // heaviest tiles first over all heads while their query forms (two, fp16) fit in L2 together
+  a.head_major = 4 * lay.rows * p->hq * D > (96LL << 20) ? 1 : 0;
   a.kweight = kweight;
   std::memcpy(a.omega, rope.omega, sizeof(a.omega));
   cudaError_t e;
   if (dtype == BF_DTYPE_BF16)
-    e = D == 128 ? launch_weights<bf16, 128>(a, st) : launch_weights<bf16, 64>(a, st);
+    e = D == 128 ? launch_weights<bf16, 128>(a, qt, st) : launch_weights<bf16, 64>(a, qt, st);
   else
-    e = D == 128 ? launch_weights<float, 128>(a, st) : launch_weights<float, 64>(a, st);
+    e = D == 128 ? launch_weights<float, 128>(a, qt, st) : launch_weights<float, 64>(a, qt, st);
   return e == cudaSuccess ? BF_OK : BF_ERR_CUDA;
 }
 

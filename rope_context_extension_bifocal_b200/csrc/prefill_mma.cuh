@@ -74,11 +74,11 @@ __global__ void __launch_bounds__(256, 1) attn_mma_kernel(const __grid_constant_
   const int h = blockIdx.y, b = PACKED ? 0 : blockIdx.z;
   if (PACKED) {
     const int rank = blockIdx.x;
+    const PackedTile tile = a.packed.tiles[rank];
     if (rank >= a.packed.head->n_tiles) return;
-    const int2 tile = a.packed.tiles[rank];
-    i0 = tile.y * BM;
-    row0 = a.packed.cu[tile.x];
-    L = a.packed.cu[tile.x + 1] - row0;
+    i0 = tile.t * BM;
+    row0 = tile.first;
+    L = tile.n;
     pitch = a.packed.total_rows;
     if (BIFOCAL && !has_long_pairs(L, factor_of(L, a.packed.w_pretrained), w0)) w0 = kAllLocal;
   } else {

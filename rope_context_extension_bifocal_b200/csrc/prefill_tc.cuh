@@ -93,6 +93,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
+// The same wait, tied to the 32 registers it completes: what uses them cannot be moved above it while
+// another load is in flight.
+__device__ __forceinline__ void wait_ld32(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+                 "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]),
+                 "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
+                 "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29])
+               :
+               : "memory");
+  asm volatile("" : "+f"(v[30]), "+f"(v[31]));
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
@@ -159,13 +171,13 @@ __global__ void __launch_bounds__(tc::NTHREADS, 1) attn_tc_kernel(const __grid_c
   int h, b, i0, L = a.L, row0 = 0, pitch = a.L, w0 = a.w0;
   if (PACKED) {
     const int rank = static_cast<int>(blockIdx.x) / a.hq;
+    const PackedTile tile = a.packed.tiles[rank];
     if (rank >= a.packed.head->n_tiles) return;
-    const int2 tile = a.packed.tiles[rank];
     h = static_cast<int>(blockIdx.x) % a.hq;
     b = 0;
-    i0 = tile.y * BM;
-    row0 = a.packed.cu[tile.x];
-    L = a.packed.cu[tile.x + 1] - row0;
+    i0 = tile.t * BM;
+    row0 = tile.first;
+    L = tile.n;
     pitch = a.packed.total_rows;
     if (BIFOCAL && !has_long_pairs(L, factor_of(L, a.packed.w_pretrained), w0)) w0 = kAllLocal;
   } else {

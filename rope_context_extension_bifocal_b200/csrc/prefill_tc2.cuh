@@ -191,14 +191,14 @@ __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __gri
     const int ppk = pairs / a.hkv;
     const int idx = static_cast<int>(blockIdx.x);
     const int rank = idx / ppk % a.packed.max_tiles;
+    const PackedTile tile = a.packed.tiles[rank];
     if (rank >= a.packed.head->n_tiles) return;
-    const int2 tile = a.packed.tiles[rank];
     hp = idx / (ppk * a.packed.max_tiles) * ppk + idx % ppk;
     b = 0;
-    qrow0 = a.packed.cu[tile.x];
-    Lq = a.packed.cu[tile.x + 1] - qrow0;
+    qrow0 = tile.first;
+    Lq = tile.n;
     q_off = 0;
-    qt = tile.y;
+    qt = tile.t;
     G = factor_of(Lq, a.packed.w_pretrained);
   } else {
     // kv-head major: the CTAs resident at one time share one kv head's K and V tiles (the key

@@ -126,6 +126,29 @@ def test_neighbours_and_earlier_queries_do_not_leak():
     bfl.last_device_error()
 
 
+def test_many_queries_use_one_product():
+    """From 16384 (query, head) rows on the operands are single fp16 values: a term is off by at most scale
+    (2^-10 + 2^-20) sum |q_d k_d| of itself, at random, so a sum of n comparable terms by that over sqrt(n). The error
+    over all keys is held to a fourteenth of the worst term's (terms average 2^-11 / sqrt(3) twice, a third of the worst
+    of it, and every key has some terms of its own to average over, the median one hundreds)."""
+    L, hq, hkv, w0, wp = 2100, 8, 1, 300, 700
+    g = si.generator(77)
+    q, k = torch.randn(L, hq, 128, generator=g).bfloat16(), torch.randn(L, hkv, 128, generator=g).bfloat16()
+    x, _ = scores(q.double().numpy(), k.double().numpy(), w0, wp, si.FREQ_INTERP, False)
+    m = x.max(2)
+    l = (m + np.log(np.exp(x - m[..., None]).sum(2))).astype(np.float32)
+    want = np.exp(x - l[..., None].astype(np.float64)).sum((0, 1))
+    # sum |q_d k_d| under any rotation is at most the sum over pairs of |q_pair| |k_pair|
+    pair = [np.linalg.norm(np.stack([y[..., :64], y[..., 64:]]), axis=0).reshape(-1, 64) for y in (q.double().numpy(), k.double().numpy())]
+    term = (2.0 ** -10 + 2.0 ** -20) / math.sqrt(128) * (pair[0] @ pair[1].T).max()
+    cu = torch.tensor([0, L], dtype=torch.int32).cuda()
+    got = bfl.bifocal_key_weights(q.cuda(), k.cuda(), torch.from_numpy(l).cuda(), cu, L, L, w0=w0, w_pretrained=wp, theta=THETA)
+    assert bfl.last_device_error() == 0
+    err = got[0].cpu().double().numpy() - want
+    assert np.all(np.abs(err) <= (term + 4e-6) * want)
+    assert np.linalg.norm(err) <= term / 14 * np.linalg.norm(want)
+
+
 def test_sum_is_the_number_of_queries():
     """With the prefill's own log-sum-exps the weights of a sequence sum to its queries times the group."""
     lens = [900, 350]
