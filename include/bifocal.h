@@ -248,7 +248,9 @@ BF_API bf_status_t bifocal_prefill_chunk_paged(const void* q, const void* k, con
  * Boundaries that are not in order, exceed total_rows or give a length above max_len are reported as
  * BF_ERR_INDEX by bifocal_last_device_error, and nothing is written. A block-table entry outside the
  * pool is reported likewise and its rows are not written; the attention does not read the cache.
- * Flags: BF_FLAG_WINDOW as for bifocal_prefill; BF_FLAG_FORCE_BIFOCAL and BF_FLAG_FUSED_ROPE change nothing.
+ * Both head sizes run on the tcgen05 kernels (two heads of a group a CTA, or one where the group is odd).
+ * Flags: BF_FLAG_WINDOW as for bifocal_prefill, with an even group and either head_dim; BF_FLAG_FORCE_BIFOCAL
+ * and BF_FLAG_FUSED_ROPE change nothing.
  * Errors: as bifocal_prefill; BF_ERR_INVALID also for NULL cu_seqlens, total_rows or max_len < 1 and bad
  * cache arguments; BF_ERR_UNSUPPORTED for BF_FLAG_MMA_SYNC. */
 BF_API size_t bifocal_prefill_packed_workspace_size(int32_t dtype, int32_t batch, int32_t total_rows,

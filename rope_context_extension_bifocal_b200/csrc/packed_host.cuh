@@ -70,14 +70,54 @@ PackedLayout packed_layout(int dtype, int batch, int T, const bf_params_t* p) {
   return w;
 }
 
-template <int D, bool BIF>
-cudaError_t launch_packed_mma(const bf::AttnArgs& a, int max_tiles, cudaStream_t st) {
-  constexpr int smem = bf::attn_mma_smem_bytes<D, BIF>();
-  auto kern = bf::attn_mma_kernel<D, BIF, true>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+// Operand forms [heads][rows][D] fp16, box (64, box_rows, 1), 128B swizzle.
+bool make_form_map(CUtensorMap* map, const void* base, int64_t rows, int heads, int D, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(heads)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(rows) * D * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Values [rows][hkv][D] bf16, box (64, 1, 128), 128B swizzle.
+bool make_value_map(CUtensorMap* map, const void* base, int64_t rows, int hkv, int D) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(hkv), static_cast<cuuint64_t>(rows), 1};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(hkv) * D * 2,
+                           static_cast<cuuint64_t>(rows) * hkv * D * 2};
+  cuuint32_t box[4] = {64, 1, 128, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename Args>
+cudaError_t launch_packed(void (*kern)(const Args), int64_t ctas, int threads, int smem, const Args& args, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<dim3(max_tiles, a.hq), bf::mma_cfg::WARPS * 32, smem, st>>>(a);
+  kern<<<static_cast<unsigned>(ctas), threads, smem, st>>>(args);
   return cudaGetLastError();
+}
+
+// The ping-pong kernel (even groups) and the single-tile kernel (odd ones), for either head size.
+template <int D>
+cudaError_t launch_packed_tc2(bool window, bool bif, const bf::Tc2Args& a, int64_t ctas, cudaStream_t st) {
+  using namespace bf::tc2;
+  auto kern = window ? bf::attn_tc2_kernel<KIND_WINDOW, false, true, D>
+              : bif  ? bf::attn_tc2_kernel<KIND_BIFOCAL, false, true, D>
+                     : bf::attn_tc2_kernel<KIND_PLAIN, false, true, D>;
+  return launch_packed(kern, ctas, NTHREADS2, bf::attn_tc2_smem_bytes(), a, st);
+}
+template <int D>
+cudaError_t launch_packed_tc(bool bif, const bf::TcArgs& a, int64_t ctas, cudaStream_t st) {
+  auto kern = bif ? bf::attn_tc_kernel<true, true, D> : bf::attn_tc_kernel<false, true, D>;
+  return launch_packed(kern, ctas, bf::tc::NTHREADS, bf::attn_tc_smem_bytes(), a, st);
 }
 
 bf_status_t prefill_packed_impl(const void* q, const void* k, const void* v, int32_t dtype, int32_t total_rows,
@@ -93,8 +133,8 @@ bf_status_t prefill_packed_impl(const void* q, const void* k, const void* v, int
       !aligned(cu_seqlens, 4) || (lse && !aligned(lse, 4)))
     return BF_ERR_INVALID;
   const bool window = (p->flags & BF_FLAG_WINDOW) != 0;
-  const bool tc2 = tc2_path(p);
-  if (window && !tc2) return BF_ERR_UNSUPPORTED;
+  const bool even = (p->hq / p->hkv) % 2 == 0;  // two heads of a group a CTA
+  if (window && !even) return BF_ERR_UNSUPPORTED;
   bf::CacheRows rows{};
   if (kcache || vcache || kpos) {
     if (!kcache || !vcache || !aligned(kcache, 16) || !aligned(vcache, 16) || (kpos && !aligned(kpos, 4)))
@@ -106,7 +146,7 @@ bf_status_t prefill_packed_impl(const void* q, const void* k, const void* v, int
   }
   const PackedLayout lay = packed_layout(dtype, batch, total_rows, p);
   if (!workspace || !aligned(workspace, 256) || ws_bytes < lay.total) return BF_ERR_WORKSPACE;
-  const int64_t per_tile = tc2 ? p->hq / 2 : p->hq;
+  const int64_t per_tile = even ? p->hq / 2 : p->hq;
   if (lay.max_tiles * per_tile > 0x7fffffffLL || p->hq > 65535) return BF_ERR_UNSUPPORTED;
   const int max_tiles = static_cast<int>(lay.max_tiles);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -165,13 +205,20 @@ bf_status_t prefill_packed_impl(const void* q, const void* k, const void* v, int
   pt.max_tiles = max_tiles;
   pt.total_rows = total_rows;
   pt.w_pretrained = p->w_pretrained;
-  if (tc2) {
+  CUtensorMap ko, kl, vm;
+  if (!make_form_map(&ko, pa.Ko, total_rows, p->hkv, D, 128) || !make_form_map(&kl, pa.Kl, total_rows, p->hkv, D, 128) ||
+      !make_value_map(&vm, vsrc, total_rows, p->hkv, D))
+    return BF_ERR_CUDA;
+  const int64_t ctas = max_tiles * per_tile;
+  if (even) {
     bf::Tc2Args ta;
     std::memset(&ta, 0, sizeof(ta));
-    if (!make_k_map(&ta.qo_map, pa.Qo, total_rows, p->hq) || !make_k_map(&ta.ql_map, pa.Ql, total_rows, p->hq) ||
-        !make_k_map(&ta.ko_map, pa.Ko, total_rows, p->hkv) || !make_k_map(&ta.kl_map, pa.Kl, total_rows, p->hkv) ||
-        !make_v_map(&ta.v_map, vsrc, total_rows, p->hkv, 1))
+    if (!make_form_map(&ta.qo_map, pa.Qo, total_rows, p->hq, D, 128) ||
+        !make_form_map(&ta.ql_map, pa.Ql, total_rows, p->hq, D, 128))
       return BF_ERR_CUDA;
+    ta.ko_map = ko;
+    ta.kl_map = kl;
+    ta.v_map = vm;
     ta.out = static_cast<bf16*>(out);
     ta.lse = lse;
     ta.hq = p->hq;
@@ -180,21 +227,13 @@ bf_status_t prefill_packed_impl(const void* q, const void* k, const void* v, int
     ta.w0 = p->w0;
     ta.scale_log2 = scale_log2(p);
     ta.packed = pt;
-    constexpr int smem = bf::attn_tc2_smem_bytes();
-    auto kern = window ? bf::attn_tc2_kernel<bf::tc2::KIND_WINDOW, false, true>
-                : bif  ? bf::attn_tc2_kernel<bf::tc2::KIND_BIFOCAL, false, true>
-                       : bf::attn_tc2_kernel<bf::tc2::KIND_PLAIN, false, true>;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) {
-      kern<<<static_cast<unsigned>(max_tiles * per_tile), bf::tc2::NTHREADS2, smem, st>>>(ta);
-      e = cudaGetLastError();
-    }
-  } else if (D == 128) {
+    e = D == 128 ? launch_packed_tc2<128>(window, bif, ta, ctas, st) : launch_packed_tc2<64>(window, bif, ta, ctas, st);
+  } else {
     bf::TcArgs ta;
     std::memset(&ta, 0, sizeof(ta));
-    if (!make_k_map(&ta.ko_map, pa.Ko, total_rows, p->hkv) || !make_k_map(&ta.kl_map, pa.Kl, total_rows, p->hkv) ||
-        !make_v_map(&ta.v_map, vsrc, total_rows, p->hkv, 1))
-      return BF_ERR_CUDA;
+    ta.ko_map = ko;
+    ta.kl_map = kl;
+    ta.v_map = vm;
     ta.Qo = pa.Qo;
     ta.Ql = pa.Ql;
     ta.out = static_cast<bf16*>(out);
@@ -204,29 +243,7 @@ bf_status_t prefill_packed_impl(const void* q, const void* k, const void* v, int
     ta.w0 = p->w0;
     ta.scale_log2 = scale_log2(p);
     ta.packed = pt;
-    constexpr int smem = bf::attn_tc_smem_bytes();
-    auto kern = bif ? bf::attn_tc_kernel<true, true> : bf::attn_tc_kernel<false, true>;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) {
-      kern<<<static_cast<unsigned>(max_tiles * per_tile), bf::tc::NTHREADS, smem, st>>>(ta);
-      e = cudaGetLastError();
-    }
-  } else {
-    bf::AttnArgs aa{};
-    aa.Qo = pa.Qo;
-    aa.Ql = pa.Ql;
-    aa.Ko = pa.Ko;
-    aa.Kl = pa.Kl;
-    aa.V = static_cast<const bf16*>(vsrc);
-    aa.v_row_stride = static_cast<long long>(p->hkv) * D;
-    aa.out = static_cast<bf16*>(out);
-    aa.lse = lse;
-    aa.hq = p->hq;
-    aa.hkv = p->hkv;
-    aa.w0 = p->w0;
-    aa.scale_log2 = scale_log2(p);
-    aa.packed = pt;
-    e = bif ? launch_packed_mma<64, true>(aa, max_tiles, st) : launch_packed_mma<64, false>(aa, max_tiles, st);
+    e = D == 128 ? launch_packed_tc<128>(bif, ta, ctas, st) : launch_packed_tc<64>(bif, ta, ctas, st);
   }
   return e == cudaSuccess ? BF_OK : BF_ERR_CUDA;
 }
@@ -466,19 +483,6 @@ WeightLayout weight_layout(int batch, int T, int obs, const bf_params_t* p) {
   w.nl = w.forms + 4 * w.form_bytes;
   w.total = w.nl + align256((static_cast<size_t>(w.rows) * (p->hq / p->hkv) + 128) * p->hkv * 4);
   return w;
-}
-
-// Query forms [kv heads][rows][D] fp16, box (64, box_rows, 1), 128B swizzle.
-bool make_form_map(CUtensorMap* map, const void* base, int64_t rows, int heads, int D, int box_rows) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(heads)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(rows) * D * 2};
-  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename Tin, int D, int QT>

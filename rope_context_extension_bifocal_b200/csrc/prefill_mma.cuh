@@ -11,7 +11,6 @@
 // forming the subtracted terms.
 #pragma once
 #include "common.cuh"
-#include "packed.cuh"
 
 namespace bf {
 
@@ -27,7 +26,6 @@ struct AttnArgs {
   float* lse;                // [b, hq, L] or null
   int L, hq, hkv, w0;
   float scale_log2;  // softmax scale * log2(e)
-  PackedTiles packed;  // PACKED only: L is then unused
 };
 
 namespace mma_cfg {
@@ -54,8 +52,7 @@ __device__ __forceinline__ void load_tile_async(uint32_t sbase, const T* g, long
   }
 }
 
-// PACKED: a batch of packed sequences; blockIdx.x is the rank in the tile list.
-template <int D, bool BIFOCAL, bool PACKED = false>
+template <int D, bool BIFOCAL>
 __global__ void __launch_bounds__(256, 1) attn_mma_kernel(const __grid_constant__ AttnArgs a) {
   using namespace mma_cfg;
   constexpr int KC = D / 16;  // k-chunks of the QK^T contraction
@@ -69,36 +66,24 @@ __global__ void __launch_bounds__(256, 1) attn_mma_kernel(const __grid_constant_
   const uint32_t sK = sQ + NV * QTILE;                   // [2 stages][NV][BN][D]
   const uint32_t sV = sK + 2 * NV * KTILE;               // [2 stages][BN][D]
 
-  // the sequence's length L; its first row row0; rows a head (pitch)
-  int i0, L = a.L, row0 = 0, pitch = a.L, w0 = a.w0;
-  const int h = blockIdx.y, b = PACKED ? 0 : blockIdx.z;
-  if (PACKED) {
-    const int rank = blockIdx.x;
-    const PackedTile tile = a.packed.tiles[rank];
-    if (rank >= a.packed.head->n_tiles) return;
-    i0 = tile.t * BM;
-    row0 = tile.first;
-    L = tile.n;
-    pitch = a.packed.total_rows;
-    if (BIFOCAL && !has_long_pairs(L, factor_of(L, a.packed.w_pretrained), w0)) w0 = kAllLocal;
-  } else {
-    const int n_qt = (a.L + BM - 1) / BM;
-    const int qt = n_qt - 1 - blockIdx.x;  // heaviest tiles first
-    i0 = qt * BM;
-  }
+  const int n_qt = (a.L + BM - 1) / BM;
+  const int qt = n_qt - 1 - blockIdx.x;  // heaviest tiles first
+  const int h = blockIdx.y, b = blockIdx.z;
   const int kvh = h / (a.hq / a.hkv);
+  const int i0 = qt * BM;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int w0 = a.w0;
 
-  const long long qoff = ((static_cast<long long>(b) * a.hq + h) * pitch + row0 + i0) * D;
-  const long long koff = ((static_cast<long long>(b) * a.hkv + kvh) * pitch + row0) * D;
-  const __nv_bfloat16* Vg = a.V + b * a.v_batch_stride + row0 * a.v_row_stride + kvh * D;
+  const long long qoff = (static_cast<long long>(b) * a.hq + h) * a.L * D + static_cast<long long>(i0) * D;
+  const long long koff = (static_cast<long long>(b) * a.hkv + kvh) * a.L * D;
+  const __nv_bfloat16* Vg = a.V + b * a.v_batch_stride + kvh * D;
 
-  const int qvalid = min(BM, L - i0);
+  const int qvalid = min(BM, a.L - i0);
   load_tile_async<D, BM>(sQ, a.Qo + qoff, D, qvalid);
   if (BIFOCAL) load_tile_async<D, BM>(sQ + QTILE, a.Ql + qoff, D, qvalid);
   cp_async_commit();
 
-  const int kv_end = min(i0 + BM, L);
+  const int kv_end = min(i0 + BM, a.L);
   const int n_kt = (kv_end + BN - 1) / BN;
 
   auto tile_needs = [&](int j0, bool& need_o, bool& need_l) {
@@ -113,7 +98,7 @@ __global__ void __launch_bounds__(256, 1) attn_mma_kernel(const __grid_constant_
   };
   auto issue_kv = [&](int t) {
     const int j0 = t * BN, st = t & 1;
-    const int valid = min(BN, L - j0);
+    const int valid = min(BN, a.L - j0);
     bool no, nl;
     tile_needs(j0, no, nl);
     const uint32_t kb = sK + st * NV * KTILE;
@@ -258,16 +243,16 @@ __global__ void __launch_bounds__(256, 1) attn_mma_kernel(const __grid_constant_
     lsum += __shfl_xor_sync(0xffffffffu, lsum, 1);
     lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
     const int i = iw + g8 + r * 8;
-    if (i < L) {
+    if (i < a.L) {
       const float inv = 1.f / lsum;
-      __nv_bfloat16* orow = a.out + ((static_cast<long long>(b) * a.L + row0 + i) * a.hq + h) * D;
+      __nv_bfloat16* orow = a.out + ((static_cast<long long>(b) * a.L + i) * a.hq + h) * D;
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) {
         const uint32_t pk = pack_bf16x2(o[dt][2 * r] * inv, o[dt][2 * r + 1] * inv);
         *reinterpret_cast<uint32_t*>(orow + dt * 8 + 2 * t4) = pk;
       }
       if (a.lse && t4 == 0)
-        a.lse[(static_cast<long long>(b) * a.hq + h) * pitch + row0 + i] = (m_r[r] + __log2f(lsum)) * 0.69314718055994530942f;
+        a.lse[(static_cast<long long>(b) * a.hq + h) * a.L + i] = (m_r[r] + __log2f(lsum)) * 0.69314718055994530942f;
     }
   }
 }

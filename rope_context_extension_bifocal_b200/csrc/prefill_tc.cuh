@@ -156,10 +156,13 @@ __device__ __forceinline__ int tile_visits(int i0, int t, int w0, int (&kinds)[2
   return 1;
 }
 
-// PACKED: a batch of packed sequences (as in attn_tc2_kernel).
-template <bool BIFOCAL, bool PACKED = false>
+// PACKED: a batch of packed sequences, of head size 128 or 64 (as in attn_tc2_kernel).
+template <bool BIFOCAL, bool PACKED = false, int HD = 128>
 __global__ void __launch_bounds__(tc::NTHREADS, 1) attn_tc_kernel(const __grid_constant__ TcArgs a) {
   using namespace tc;
+  static_assert(HD == 128 || (HD == 64 && PACKED), "head size 64 is built for packed batches");
+  constexpr uint32_t TILE_BYTES = HD == 128 ? SLOT_BYTES : HALF_BYTES;
+  constexpr uint32_t IDESC_O = HD == 128 ? IDESC_PV : IDESC_PV - (8u << 17);  // N = 128 or 64
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint64_t full[NSLOT], empty[NSLOT], s_full[2], p_ready[2], o_done, q_ready, mma_drain;
   __shared__ uint32_t tmem_base_sh;
@@ -237,15 +240,15 @@ __global__ void __launch_bounds__(tc::NTHREADS, 1) attn_tc_kernel(const __grid_c
               ok = false;
               break;
             }
-            mbar_arrive_expect_tx(&full[slot], SLOT_BYTES);
+            mbar_arrive_expect_tx(&full[slot], TILE_BYTES);
             uint8_t* dst = smem + slot * SLOT_BYTES;
             if (x == 0) {
               const CUtensorMap* m = lng ? &a.kl_map : &a.ko_map;
               tma_load_3d(dst, m, &full[slot], 0, row0 + t * BN, krow);
-              tma_load_3d(dst + HALF_BYTES, m, &full[slot], 64, row0 + t * BN, krow);
+              if (HD == 128) tma_load_3d(dst + HALF_BYTES, m, &full[slot], 64, row0 + t * BN, krow);
             } else {
               tma_load_4d(dst, &a.v_map, &full[slot], 0, kvh, row0 + t * BN, b);
-              tma_load_4d(dst + HALF_BYTES, &a.v_map, &full[slot], 64, kvh, row0 + t * BN, b);
+              if (HD == 128) tma_load_4d(dst + HALF_BYTES, &a.v_map, &full[slot], 64, kvh, row0 + t * BN, b);
             }
           }
         }
@@ -280,7 +283,7 @@ __global__ void __launch_bounds__(tc::NTHREADS, 1) attn_tc_kernel(const __grid_c
           // arithmetic between the K-steps would stretch the group
           const uint64_t kd0 = k_desc(kslot, 0);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
+          for (int kk = 0; kk < HD / 16; ++kk)
             mma_ts(s_col, q_col + kk * 8, kd0 + (((kk >> 2) * HALF_BYTES + (kk & 3) * 32) >> 4), IDESC_QK, kk > 0);
           mma_commit(&s_full[v & 1]);
           mma_commit(&empty[ks]);
@@ -298,7 +301,7 @@ __global__ void __launch_bounds__(tc::NTHREADS, 1) attn_tc_kernel(const __grid_c
             const uint32_t acc0 = v - 1 > 0;
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              mma_ts(tmem + COL_O, p_col + kk * 8, vd0 + kk * (2048 >> 4), IDESC_PV, kk > 0 ? 1u : acc0);
+              mma_ts(tmem + COL_O, p_col + kk * 8, vd0 + kk * (2048 >> 4), IDESC_O, kk > 0 ? 1u : acc0);
             mma_commit(&empty[prev_vslot]);
             mma_commit(&o_done);
           }
@@ -316,7 +319,7 @@ __global__ void __launch_bounds__(tc::NTHREADS, 1) attn_tc_kernel(const __grid_c
           const uint32_t acc0 = v - 1 > 0;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ts(tmem + COL_O, p_col + kk * 8, vd0 + kk * (2048 >> 4), IDESC_PV, kk > 0 ? 1u : acc0);
+            mma_ts(tmem + COL_O, p_col + kk * 8, vd0 + kk * (2048 >> 4), IDESC_O, kk > 0 ? 1u : acc0);
           mma_commit(&empty[prev_vslot]);
           mma_commit(&o_done);
         }
@@ -336,8 +339,8 @@ __global__ void __launch_bounds__(tc::NTHREADS, 1) attn_tc_kernel(const __grid_c
     // Q (both RoPE forms) into TMEM: lane = row, 64 columns of fp16 pairs each; each half
     // of the row's threads writes 32 columns of each form
     {
-      const long long qrow = ((static_cast<long long>(b) * a.hq + h) * pitch + row0 + i) * D;
-      for (int f = 0; f < (BIFOCAL ? 2 : 1); ++f) {
+      const long long qrow = ((static_cast<long long>(b) * a.hq + h) * pitch + row0 + i) * HD;
+      for (int f = 0; f < (BIFOCAL ? 2 : 1) && (HD == 128 || half == 0); ++f) {
         const __half* src = (f == 0 ? a.Qo : a.Ql) + qrow;
         const int c0 = 32 * half;
         uint32_t reg[32];
@@ -437,9 +440,9 @@ __global__ void __launch_bounds__(tc::NTHREADS, 1) attn_tc_kernel(const __grid_c
             // warp-uniform: rescale this half of O if any row of the warp needs it (others scale by 1)
             if (__any_sync(0xffffffffu, grow)) {
               const float f = grow ? alpha : 1.f;
-              const uint32_t o_addr = lane_addr + COL_O + 64 * half;
+              const uint32_t o_addr = lane_addr + COL_O + HD / 2 * half;
 #pragma unroll 1
-              for (int c = 0; c < 64; c += 32) {
+              for (int c = 0; c < HD / 2; c += 32) {
                 float ov[32];
                 tmem_ld32(o_addr + c, ov);
                 wait_ld();
@@ -476,11 +479,11 @@ __global__ void __launch_bounds__(tc::NTHREADS, 1) attn_tc_kernel(const __grid_c
     if (fin) {
       fence_after();
       const float inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
-      __nv_bfloat16* orow = a.out + ((static_cast<long long>(b) * a.L + row0 + i) * a.hq + h) * D + 64 * half;
+      __nv_bfloat16* orow = a.out + ((static_cast<long long>(b) * a.L + row0 + i) * a.hq + h) * HD + HD / 2 * half;
 #pragma unroll 1
-      for (int c = 0; c < 64; c += 32) {
+      for (int c = 0; c < HD / 2; c += 32) {
         float ov[32];
-        tmem_ld32(lane_addr + COL_O + 64 * half + c, ov);
+        tmem_ld32(lane_addr + COL_O + HD / 2 * half + c, ov);
         wait_ld();
         if (i < L) {
 #pragma unroll

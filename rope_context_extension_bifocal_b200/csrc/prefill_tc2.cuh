@@ -154,9 +154,14 @@ struct Tc2Args {
 // PACKED = true (unfused): a batch of packed sequences. Q, K and V rows are packed rows, a CTA's
 // query tile comes from the tile list, and value rows past the sequence's end (the next
 // sequence's, or no one's) are zeroed in shared memory before the last P.V reads them.
-template <int KIND, bool FUSED, bool PACKED = false>
+// HD = 64 (packed only): head size 64 on the same layout, each tile in the first half of its slot, half the
+// K-steps of QK^T and 64 columns of O.
+template <int KIND, bool FUSED, bool PACKED = false, int HD = 128>
 __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __grid_constant__ Tc2Args a) {
   using namespace tc2;
+  static_assert(HD == 128 || (HD == 64 && PACKED && !FUSED), "head size 64 is built for packed batches");
+  constexpr uint32_t TILE_BYTES = HD == 128 ? SLOT_BYTES : HALF_BYTES;  // of a slot, what a tile fills
+  constexpr uint32_t IDESC_O = HD == 128 ? IDESC_PV : IDESC_PV - (8u << 17);  // N = 128 or 64
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint64_t full[NSLOT2], empty[NSLOT2], s_full[2], p_ready[2], o_done[2], q_full, q_free, mma_drain;
   // P is handed over in two halves (keys 0-63, 64-127 of the tile): p_lo releases the first
@@ -314,7 +319,7 @@ __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __gri
         // Q: both heads; fused: raw rows of this call (map over Lq rows), else the rotated form
         auto load_q = [&](bool lng) {
           uint64_t* bar = FUSED ? &q_raw : &q_full;
-          mbar_arrive_expect_tx(bar, 2 * Q_BYTES);
+          mbar_arrive_expect_tx(bar, 2 * TILE_BYTES);
           for (int x = 0; x < 2; ++x) {
             uint8_t* dst = smem + x * Q_BYTES;
             if (FUSED) {
@@ -326,7 +331,7 @@ __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __gri
               const CUtensorMap* m = lng ? &a.ql_map : &a.qo_map;
               const int row = (PACKED ? qrow0 : 0) + qt * BM;
               tma_load_3d(dst, m, bar, 0, row, b * a.hq + h0 + x);
-              tma_load_3d(dst + HALF_BYTES, m, bar, 64, row, b * a.hq + h0 + x);
+              if (HD == 128) tma_load_3d(dst + HALF_BYTES, m, bar, 64, row, b * a.hq + h0 + x);
             }
           }
         };
@@ -380,17 +385,17 @@ __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __gri
             }
             return true;
           }
-          mbar_arrive_expect_tx(bar, SLOT_BYTES);
+          mbar_arrive_expect_tx(bar, TILE_BYTES);
           if (x == 1 || FUSED) {
             const CUtensorMap* m = x == 0 ? &a.ko_map : &a.v_map;
             const int row = (PACKED ? qrow0 : 0) + t * BN;
             tma_load_4d(dst, m, bar, 0, kvh, row, b);
-            tma_load_4d(dst + HALF_BYTES, m, bar, 64, kvh, row, b);
+            if (HD == 128) tma_load_4d(dst + HALF_BYTES, m, bar, 64, kvh, row, b);
           } else {
             const CUtensorMap* m = lng ? &a.kl_map : &a.ko_map;
             const int row = (PACKED ? qrow0 : 0) + t * BN;
             tma_load_3d(dst, m, bar, 0, row, krow);
-            tma_load_3d(dst + HALF_BYTES, m, bar, 64, row, krow);
+            if (HD == 128) tma_load_3d(dst + HALF_BYTES, m, bar, 64, row, krow);
           }
           return true;
         };
@@ -510,7 +515,7 @@ __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __gri
           const uint64_t b0 = dk0 + static_cast<uint64_t>(k_slot(v) * (SLOT_BYTES >> 4));
           const uint32_t d = tmem + (x == 0 ? COL_SA : COL_SB);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
+          for (int kk = 0; kk < HD / 16; ++kk) {
             const uint64_t step = ((kk >> 2) * HALF_BYTES + (kk & 3) * 32) >> 4;
             mma_ss(d, a0 + step, b0 + step, IDESC_QK, kk > 0);
           }
@@ -525,7 +530,7 @@ __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __gri
 #pragma unroll
           for (int k4 = 0; k4 < 4; ++k4) {
             const int kk = 4 * h + k4;
-            mma_ts(o_col, p_col + kk * 8, b0 + static_cast<uint64_t>(kk * (2048 >> 4)), IDESC_PV, kk > 0 ? 1u : acc0);
+            mma_ts(o_col, p_col + kk * 8, b0 + static_cast<uint64_t>(kk * (2048 >> 4)), IDESC_O, kk > 0 ? 1u : acc0);
           }
           mma_commit(h == 0 ? &o_lo[x] : &o_done[x]);
         };
@@ -720,7 +725,7 @@ __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __gri
             if (__any_sync(0xffffffffu, grow)) {  // warp-uniform; rows that need none scale by 1
               const float f = grow ? alpha : 1.f;
 #pragma unroll 1
-              for (int c0 = 0; c0 < 128; c0 += 32) {
+              for (int c0 = 0; c0 < HD; c0 += 32) {
                 float ov[32];
                 tmem_ld32(o_col + c0, ov);
                 wait_ld();
@@ -802,7 +807,7 @@ __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __gri
           if (__any_sync(0xffffffffu, grow)) {  // warp-uniform; rows that need none scale by 1
             const float f = grow ? alpha : 1.f;
 #pragma unroll 1
-            for (int c0 = 0; c0 < 128; c0 += 32) {
+            for (int c0 = 0; c0 < HD; c0 += 32) {
               float ov[32];
               tmem_ld32(o_col + c0, ov);
               wait_ld();
@@ -840,9 +845,9 @@ __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __gri
       fence_after();
       const float inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
       const int rel = i - q_off;  // row of this query in the call's rows
-      __nv_bfloat16* orow = a.out + ((static_cast<long long>(qrow0) + rel) * a.hq + h) * D;
+      __nv_bfloat16* orow = a.out + ((static_cast<long long>(qrow0) + rel) * a.hq + h) * HD;
 #pragma unroll 1
-      for (int c0 = 0; c0 < 128; c0 += 32) {
+      for (int c0 = 0; c0 < HD; c0 += 32) {
         float ov[32];
         tmem_ld32(o_col + c0, ov);
         wait_ld();

@@ -87,6 +87,8 @@ CASES = [
     ([260, 100], 4, 2, 128, torch.bfloat16, 500, 1000, si.FREQ_INTERP),    # G = 1 throughout: the plain kernel
     ([260, 100, 300], 4, 2, 64, torch.bfloat16, 40, 280, si.FREQ_INTERP),  # G = 1 and 2 in one call
     ([260, 100, 300], 3, 1, 128, torch.bfloat16, 40, 280, si.POS_ALIAS),
+    ([300, 63, 640], 8, 2, 64, torch.bfloat16, 130, 90, si.POS_ALIAS),     # D = 64, two heads a CTA
+    ([1, 385], 5, 1, 64, torch.float32, 33, 100, si.FREQ_INTERP),          # D = 64, five heads a group
 ]
 
 
@@ -100,16 +102,17 @@ def test_matches_oracle(case):
     check(lens, x, cu, out, lse, w0, wp, mode)
 
 
-def test_window():
+@pytest.mark.parametrize("D", [64, 128])
+def test_window(D):
     lens = [5, 300, 0, 129]
-    x, cu = make(lens, 4, 2, 128, torch.bfloat16, 77)
+    x, cu = make(lens, 4, 2, D, torch.bfloat16, 77)
     out, lse = bfl.bifocal_prefill_packed(*(t.cuda() for t in x), cu.cuda(), 300, w0=40, w_pretrained=64, theta=THETA,
                                           flags=bfl.FLAG_WINDOW)
     assert bfl.last_device_error() == 0
     check(lens, x, cu, out, lse, 40, 64, si.FREQ_INTERP, window=True)
 
 
-@pytest.mark.parametrize("hq,hkv,D", [(4, 2, 128), (3, 1, 128), (4, 2, 64)])
+@pytest.mark.parametrize("hq,hkv,D", [(4, 2, 128), (3, 1, 128), (4, 2, 64), (3, 3, 64)])
 def test_neighbours_do_not_leak(hq, hkv, D):
     """Sequences beside NaN and infinite ones give, bit for bit, what they give alone."""
     lens = [70, 200, 64, 129, 31]

@@ -35,10 +35,9 @@ def test_prefill_packed_validation(lib):
                 dict(kc=FAKE, vc=FAKE, rows=1 << 31, table=None)):
         assert call(**bad) == INVALID, bad
     for bad in (dict(dtype=5), dict(p=params(head_dim=96)), dict(p=params(flags=bfl.FLAG_MMA_SYNC)),
-                dict(p=params(flags=bfl.FLAG_WINDOW, w0=8, hq=24)),
-                dict(p=params(flags=bfl.FLAG_WINDOW, w0=8, head_dim=64))):
+                dict(p=params(flags=bfl.FLAG_WINDOW, w0=8, hq=24))):
         assert call(**bad) == UNSUPPORTED, bad
-    for good in (dict(kc=FAKE, vc=FAKE, rows=100), dict(kc=FAKE, vc=FAKE, rows=96, table=FAKE, page=48, max_pages=2)):
+    for good in (dict(p=params(flags=bfl.FLAG_WINDOW, w0=8, head_dim=64)), dict(kc=FAKE, vc=FAKE, rows=100), dict(kc=FAKE, vc=FAKE, rows=96, table=FAKE, page=48, max_pages=2)):
         assert call(**good) == WORKSPACE, good
 
 
