@@ -39,6 +39,7 @@
 namespace bf {
 
 namespace kw {
+constexpr int QROWS = 4;  // query rows a CTA of weights_query_kernel
 constexpr int NBUF = 4;   // S tiles in tensor memory, and log-sum-exp rows in shared memory
 constexpr int NTHREADS = 320;
 constexpr uint32_t HALF = 16384;    // 128 rows of 64 fp16 values
@@ -52,12 +53,10 @@ struct WeightArgs {
   const void* q;
   const void* k;      // [T, hkv, D] raw
   const float* lse;   // [hq, T]
-  const int* cu;
-  const PlanHeader* head;
-  const PackedTile* tiles;
-  const int* qoff;    // [batch + 1] first query of a sequence in the forms
-  int batch, total_rows, hq, hkv, max_tiles;
-  int obs, w0, w_pretrained, mode, window;
+  PlanArgs plan;
+  int hq, hkv;
+  int window_pitch;   // queries set aside for a sequence in the forms; 0: as many as it has rows
+  int w0, w_pretrained, mode, window;
   int head_major;     // CTAs in the order of kv heads (their query forms share L2), or of work alone
   __half* forms[4];   // the forms above, as weights_query_kernel writes them: Qo high, low, Ql high, low
   float* nl;          // [hkv][nl_pitch] -lse * log2(e) of the rows of the forms
@@ -69,85 +68,123 @@ struct WeightArgs {
   double omega[64];
 };
 
-__device__ __forceinline__ void split_f16(const float (&x)[8], uint4& hi, uint4& lo, bool& fin) {
-  uint32_t h[4], l[4];
+// A value as an fp16 and the fp16 rest; `top` as in to_f16.
+__device__ __forceinline__ void split_f16(const float (&x)[8], uint4& hi, uint4& lo, __half2& top) {
+  hi = to_f16(x, top);
+  const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w};
+  uint32_t l[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    fin &= f16_ok(x[2 * e]) & f16_ok(x[2 * e + 1]);
-    h[e] = pack_f16x2(x[2 * e], x[2 * e + 1]);
-    const __half2 v = *reinterpret_cast<const __half2*>(&h[e]);
-    const float2 f = __half22float2(v);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[e]));
     l[e] = pack_f16x2(x[2 * e] - f.x, x[2 * e + 1] - f.y);
   }
-  hi = make_uint4(h[0], h[1], h[2], h[3]);
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// Query forms of the rows that count: a warp for a query and every gridDim.y-th four heads (8 lanes a head, 8
-// pairs a lane). Many rows take all heads in one warp, which then forms its angles once; few rows are spread
-// over more warps instead, since their time is latency.
+// First query of sequence b in the forms, a multiple of four so that a tile's log-sum-exps start on a 16-byte
+// boundary: window_pitch queries a sequence, or the sequence's own rows with room for the rounding.
+__device__ __forceinline__ int first_query(const WeightArgs& a, int b, int first) {
+  return a.window_pitch ? b * a.window_pitch : (first + 3 * b + 3) & ~3;
+}
+
+// Query forms of the rows that count. A CTA takes QROWS of them (the first CTA makes the tile list): as in
+// rope_packed_kernel it looks them up, evaluates their angles once, and deals (row, four heads) units to its warps.
 template <typename Tin, int D>
-__global__ void __launch_bounds__(256) weights_query_kernel(const __grid_constant__ WeightArgs a) {
+__global__ void __launch_bounds__(kPlanThreads) weights_query_kernel(const __grid_constant__ WeightArgs a) {
   constexpr int P = D / 2;
-  constexpr int LANES_PER_ROW = P / 8;
+  constexpr int LPR = P / 8;
+  constexpr int UNITS = 2;
+  struct Row {
+    int w, r, p, G, lng, low;  // query of the forms (-1: none), packed row, position, factor, forms wanted
+  };
+  __shared__ Row s_row[kw::QROWS];
+  __shared__ float4 s_cs[kw::QROWS][2][4][LPR];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
   pdl_wait();
-  const int w = blockIdx.x * 8 + warp;
-  if (!a.head->ok || w >= a.qoff[a.batch]) return;
-  const int b = sequence_of(a.qoff, a.batch, w);
-  if (b < 0) return;
-  const int first = a.cu[b], n = a.cu[b + 1] - first, cnt = window_rows(n, a.obs);
-  const int i = w - a.qoff[b];
-  if (i >= cnt) return;  // padding up to a multiple of four
-  const int p = n - cnt + i, r = first + p;
-  const int G = factor_of(n, a.w_pretrained), g = a.hq / a.hkv;
-  const bool lng = !a.window && has_long_pairs(n, G, a.w0);
-  const int grp = lane >> 3, l8 = lane & 7;
-  if (l8 >= LANES_PER_ROW) return;
-  const int k0 = l8 * 8;
-  float c[2][8], s[2][8];
-  for (int f = 0; f < (lng ? 2 : 1); ++f) {
-    const int m = f == 1 && a.mode != 0 ? p / G : p;
-    const float mf = static_cast<float>(m);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const double om = a.omega[k0 + e];
-      turn_cos_sin(m, mf, turn_step(f == 1 && a.mode == 0 ? om / G : om), f ? c[1][e] : c[0][e], f ? s[1][e] : s[0][e]);
-    }
+  const bool ok = boundaries_ok(a.plan);
+  if (blockIdx.x == 0) {
+    plan_tiles(a.plan, ok);
+    return;
   }
-  const bool low = static_cast<long long>(cnt) * g < kw::SINGLE_FROM;
-  bool fin = true;
-  for (int h = blockIdx.y * 4 + grp; h < a.hq; h += gridDim.y * 4) {
-    const int kvh = h / g;
-    const long long row = static_cast<long long>(w) * g + h % g;  // of this kv head's rows
-    if (l8 == 0)
-      a.nl[kvh * a.nl_pitch + row] = -a.lse[static_cast<long long>(h) * a.total_rows + r] * 1.44269504088896340736f;
-    const Tin* src = static_cast<const Tin*>(a.q) + (static_cast<long long>(r) * a.hq + h) * D;
-    Vec8<Tin> x1, x2;
-    x1.load(src + k0);
-    x2.load(src + P + k0);
-    const long long at = (static_cast<long long>(kvh) * a.form_rows * g + row) * D;
-#pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      if (f == 1 && !lng) break;
-      float y1[8], y2[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float u = x1.get(e), v = x2.get(e);
-        y1[e] = u * c[f][e] - v * s[f][e];
-        y2[e] = v * c[f][e] + u * s[f][e];
+  if (!ok) return;
+  const int g = a.hq / a.hkv;
+  if (threadIdx.x < kw::QROWS) {
+    Row x;
+    x.w = -1;
+    const int u = (blockIdx.x - 1) * kw::QROWS + threadIdx.x;  // of the windows, or a packed row
+    const int b = a.window_pitch ? u / a.window_pitch : u < a.plan.total_rows ? sequence_of(a.plan.cu, a.plan.batch, u) : -1;
+    if (b >= 0 && b < a.plan.batch) {
+      const int first = a.plan.cu[b], n = a.plan.cu[b + 1] - first, cnt = window_rows(n, a.plan.obs);
+      const int i = a.window_pitch ? u % a.window_pitch : u - first - (n - cnt);
+      if (i >= 0 && i < cnt) {
+        x.w = first_query(a, b, first) + i;
+        x.p = n - cnt + i;
+        x.r = first + x.p;
+        x.G = factor_of(n, a.w_pretrained);
+        x.lng = !a.window && has_long_pairs(n, x.G, a.w0);
+        x.low = static_cast<long long>(cnt) * g < kw::SINGLE_FROM;
       }
-      uint4 hi, lo;
-      split_f16(y1, hi, lo, fin);
-      *reinterpret_cast<uint4*>(a.forms[2 * f] + at + k0) = hi;
-      if (low) *reinterpret_cast<uint4*>(a.forms[2 * f + 1] + at + k0) = lo;
-      split_f16(y2, hi, lo, fin);
-      *reinterpret_cast<uint4*>(a.forms[2 * f] + at + P + k0) = hi;
-      if (low) *reinterpret_cast<uint4*>(a.forms[2 * f + 1] + at + P + k0) = lo;
+    }
+    s_row[threadIdx.x] = x;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kw::QROWS * 2 * P; i += kPlanThreads) {
+    const int rr = i / (2 * P), f = i / P % 2, k = i % P;
+    const Row x = s_row[rr];
+    if (x.w < 0 || (f == 1 && !x.lng)) continue;
+    const double om = a.omega[k];
+    float c, s;
+    angle_cos_sin(f == 0        ? static_cast<double>(x.p) * om
+                  : a.mode == 0 ? static_cast<double>(x.p) * (om / x.G)
+                                : static_cast<double>(x.p / x.G) * om,
+                  c, s);
+    reinterpret_cast<float2*>(&s_cs[rr][f][k % 8 / 2][k / 8])[k % 2] = make_float2(c, s);
+  }
+  __syncthreads();
+  const int grp = lane >> 3, l8 = lane & 7;
+  if (l8 >= LPR) return;
+  const int k0 = l8 * 8, per_row = (a.hq + 3) / 4, n_units = kw::QROWS * per_row;
+  __half2 top = __float2half2_rn(0.f);
+  for (int u0 = warp; u0 < n_units; u0 += 8 * UNITS) {
+    Vec8<Tin> x1[UNITS], x2[UNITS];
+    float lse[UNITS];
+    int row_of[UNITS];
+#pragma unroll
+    for (int j = 0; j < UNITS; ++j) {
+      const int u = u0 + 8 * j, rr = u / per_row, h = u % per_row * 4 + grp;
+      row_of[j] = -1;
+      if (u >= n_units || h >= a.hq || s_row[rr].w < 0) continue;
+      row_of[j] = rr;
+      const Tin* src = static_cast<const Tin*>(a.q) + (static_cast<long long>(s_row[rr].r) * a.hq + h) * D;
+      x1[j].load(src + k0);
+      x2[j].load(src + P + k0);
+      lse[j] = l8 == 0 ? a.lse[static_cast<long long>(h) * a.plan.total_rows + s_row[rr].r] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < UNITS; ++j) {
+      if (row_of[j] < 0) continue;
+      const Row x = s_row[row_of[j]];
+      const int h = (u0 + 8 * j) % per_row * 4 + grp, kvh = h / g;
+      const long long row = static_cast<long long>(x.w) * g + h % g;  // of this kv head's rows
+      if (l8 == 0) a.nl[kvh * a.nl_pitch + row] = -lse[j] * 1.44269504088896340736f;
+      const long long at = (static_cast<long long>(kvh) * a.form_rows * g + row) * D;
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        if (f == 1 && !x.lng) break;
+        float y1[8], y2[8];
+        turn8(x1[j], x2[j], s_cs[row_of[j]][f], l8, y1, y2);
+        uint4 hi, lo;
+        split_f16(y1, hi, lo, top);
+        *reinterpret_cast<uint4*>(a.forms[2 * f] + at + k0) = hi;
+        if (x.low) *reinterpret_cast<uint4*>(a.forms[2 * f + 1] + at + k0) = lo;
+        split_f16(y2, hi, lo, top);
+        *reinterpret_cast<uint4*>(a.forms[2 * f] + at + P + k0) = hi;
+        if (x.low) *reinterpret_cast<uint4*>(a.forms[2 * f + 1] + at + P + k0) = lo;
+      }
     }
   }
-  if (!fin) report_status(kDevRange, 90);
+  if (!all_finite(top)) report_status(kDevRange, 90);
 }
 
 // 2^x of two values on the FMA pipe: x = n + f with n the nearest integer (Cody and Waite's reduction, the
@@ -201,18 +238,19 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
   pdl_launch_dependents();
   pdl_wait();
   const int idx = static_cast<int>(blockIdx.x);
-  const int kvh = a.head_major ? idx / a.max_tiles : idx % a.hkv, rank = a.head_major ? idx % a.max_tiles : idx / a.hkv;
-  const PackedTile tile = a.tiles[rank];
-  if (rank >= a.head->n_tiles) return;
+  const int kvh = a.head_major ? idx / a.plan.max_tiles : idx % a.hkv;
+  const int rank = a.head_major ? idx % a.plan.max_tiles : idx / a.hkv;
+  const PackedTile tile = a.plan.tiles[rank];
+  if (rank >= a.plan.head->n_tiles) return;
   const int g = a.hq / a.hkv;
   const int L = tile.n;
-  const int cnt = window_rows(L, a.obs), start = L - cnt;  // queries start .. L - 1
+  const int cnt = window_rows(L, a.plan.obs), start = L - cnt;  // queries start .. L - 1
   const int j0 = tile.t * 128;
   const int G = factor_of(L, a.w_pretrained);
   const bool lng_pairs = !a.window && has_long_pairs(L, G, a.w0);
   const int w0 = (a.window || lng_pairs) ? a.w0 : kAllLocal;
   const int rows = cnt * g;              // (query, head) rows
-  const int qrow = tile.qoff * g;        // their first row in the forms
+  const int qrow = first_query(a, tile.seq, tile.first) * g;  // their first row in the forms
   const bool split = rows < SINGLE_FROM;
   const int fpv = split ? 2 : 1;         // ring fills a visit
   // Query tile t holds rows QT t .. QT t + QT - 1: queries start + QT t / g .. start + (QT t + QT - 1) / g. Tiles
@@ -343,7 +381,7 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
     // The key tile under one branch, split in two: a thread has 8 pairs of every (256 / CPR)-th row; rows past the
     // sequence are zero. The loads of RB rows are in flight together.
     auto form_keys = [&](bool lng) {
-      bool fin = true;
+      __half2 top = __float2half2_rn(0.f);
       constexpr int CPR = P / 8;               // threads a row
       constexpr int RPT = 128 * CPR / 256;     // rows a thread
       constexpr int RB = sizeof(Tin) == 2 ? RPT : RPT / 2;
@@ -379,15 +417,15 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
           // element d of a row: half d / 64, 16-byte chunk (d % 64) / 8 of its 128 bytes, swizzled
           const uint32_t o1 = (k0 / 64) * HALF + sw128(row, (k0 % 64) / 8), o2 = (d2 / 64) * HALF + sw128(row, (d2 % 64) / 8);
           uint4 hi, lo;
-          split_f16(y1, hi, lo, fin);
+          split_f16(y1, hi, lo, top);
           *reinterpret_cast<uint4*>(smem + o1) = hi;
           if (split) *reinterpret_cast<uint4*>(smem + KTILE + o1) = lo;
-          split_f16(y2, hi, lo, fin);
+          split_f16(y2, hi, lo, top);
           *reinterpret_cast<uint4*>(smem + o2) = hi;
           if (split) *reinterpret_cast<uint4*>(smem + KTILE + o2) = lo;
         }
       }
-      if (!fin) report_status(kDevRange, 91);
+      if (!all_finite(top)) report_status(kDevRange, 91);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&k_ready);

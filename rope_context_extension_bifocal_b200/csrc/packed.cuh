@@ -1,12 +1,14 @@
 // Packed batches: sequences of different lengths laid one after another in [T, heads, D], their
 // boundaries in a device array cu_seqlens [batch + 1].
 //
-// packed_plan_kernel turns the boundaries into a list of 128-row tiles, the ones with the most
-// work first, that the attention kernels' CTAs index; rope_packed_kernel is the RoPE pass over
-// the packed rows (each row's position, and the factor G of its sequence, from the boundaries).
+// plan_tiles turns the boundaries into a list of 128-row tiles, the ones with the most work first, that
+// the attention kernels' CTAs index; it is one CTA's work and rides along with the pass that precedes
+// them. rope_packed_kernel is the RoPE pass over the packed rows (each row's position, and the factor G of
+// its sequence, from the boundaries).
 #pragma once
 #include "common.cuh"
 #include "rope_prepass.cuh"
+
 
 namespace bf {
 
@@ -28,16 +30,16 @@ __device__ __forceinline__ long long cache_row(const CacheRows& c, int b, int p,
 
 struct PlanHeader {
   int n_tiles;  // entries of the tile list; 0 when the boundaries are not valid
-  int ok;
 };
 
 // One 128-row tile of a sequence: its index t within the sequence, the sequence's first row and its
-// length, and (key tiles) the first row of its queries in the query forms. All a CTA needs, in one load.
-struct __align__(32) PackedTile {
-  int seq, t, first, n, qoff, pad[3];
+// length. All a CTA needs, in one load.
+struct __align__(16) PackedTile {
+  int seq, t, first, n;
 };
 
 constexpr int kPlanLevels = 1024;
+constexpr int kPlanThreads = 256;
 
 struct PlanArgs {
   const int* cu;  // [batch + 1]
@@ -46,56 +48,57 @@ struct PlanArgs {
   PlanHeader* head;
   PackedTile* tiles;
   int max_tiles;
-  int* qoff;      // key tiles: [batch + 1] first row of each sequence's queries in the query forms
 };
 
-// Queries of a sequence of n rows, and the rows they take in the query forms: a multiple of four,
-// so that a tile's log-sum-exps (4 bytes a row) start on a 16-byte boundary.
+// Queries of a sequence of n rows.
 __host__ __device__ __forceinline__ int window_rows(int n, int obs) { return n < obs ? n : obs; }
-__host__ __device__ __forceinline__ int window_pad(int n, int obs) { return (window_rows(n, obs) + 3) & ~3; }
 
-// One CTA. Checks the boundaries (each in order, no sequence longer than max_len, none past the
-// last row), then sorts the tiles by work with a counting sort over kPlanLevels levels: a query
-// tile's work grows with its index, a key tile's with the query tiles that see it. The order
-// within a level is left to the atomics: no result depends on it, only when a tile runs.
-__global__ void __launch_bounds__(1024) packed_plan_kernel(const __grid_constant__ PlanArgs a) {
-  __shared__ int hist[kPlanLevels];
-  __shared__ int wsum[32];
-  __shared__ int carry;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_launch_dependents();
-  pdl_wait();
+// Whether the boundaries are in order, no sequence longer than max_len and none past the last row. Every CTA of
+// the pass that writes cache rows asks for itself (a coalesced read of the array, in L2), so that nothing at all
+// is written for a batch with one bad boundary and the pass need not wait for a kernel that checks. All threads.
+__device__ __forceinline__ bool boundaries_ok(const PlanArgs& a) {
   bool bad = false;
-  for (int b = tid; b < a.batch; b += 1024) {
+  for (int b = threadIdx.x; b < a.batch; b += kPlanThreads) {
     const int s = a.cu[b], e = a.cu[b + 1];
     bad |= s < 0 || e < s || e > a.total_rows || e - s > a.max_len;
   }
-  hist[tid] = 0;
-  if (tid == 0) carry = 0;
-  if (__syncthreads_or(bad)) {
+  return !__syncthreads_or(bad);
+}
+
+// The tile list, by one CTA of kPlanThreads threads: the tiles sorted by work with a counting sort over
+// kPlanLevels levels. A query tile's work grows with its index, a key tile's with the queries that see it. The
+// order within a level is left to the atomics: no result depends on it, only when a tile runs.
+__device__ __forceinline__ void plan_tiles(const PlanArgs& a, bool ok) {
+  __shared__ int hist[kPlanLevels];
+  __shared__ int wsum[kPlanThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (!ok) {
     if (tid == 0) {
       report_status(kDevIndex, 60);
       a.head->n_tiles = 0;
-      a.head->ok = 0;
     }
     return;
   }
+  constexpr int PER = kPlanLevels / kPlanThreads;
+  for (int i = tid; i < kPlanLevels; i += kPlanThreads) hist[i] = 0;
+  __syncthreads();
   auto level = [&](int n, int t) {
     if (a.obs == 0) return min(t, kPlanLevels - 1);
     const int first = max(n - window_rows(n, a.obs), t * 128);
     return min((n - first + 127) / 128, kPlanLevels - 1);
   };
   // a warp per sequence, a lane per tile
-  for (int b = warp; b < a.batch; b += 32) {
+  for (int b = warp; b < a.batch; b += kPlanThreads / 32) {
     const int n = a.cu[b + 1] - a.cu[b];
     for (int t = lane; t * 128LL < n; t += 32) atomicAdd(&hist[level(n, t)], 1);
   }
   __syncthreads();
-  // exclusive scan from the top level down: where each level's tiles start
+  // exclusive scan from the top level down: where each level's tiles start (PER levels a thread)
   {
-    const int lv = kPlanLevels - 1 - tid;
-    const int c = hist[lv];
-    int x = c;
+    int c[PER], sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) sum += c[i] = hist[kPlanLevels - 1 - (tid * PER + i)];
+    int x = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -103,53 +106,21 @@ __global__ void __launch_bounds__(1024) packed_plan_kernel(const __grid_constant
     }
     if (lane == 31) wsum[warp] = x;
     __syncthreads();
-    if (warp == 0) {
-      int w = wsum[lane];
+    for (int w = 0; w < warp; ++w) x += wsum[w];
+    if (tid == kPlanThreads - 1) a.head->n_tiles = min(x, a.max_tiles);
+    x -= sum;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += y;
-      }
-      wsum[lane] = w;
-    }
-    __syncthreads();
-    const int incl = x + (warp ? wsum[warp - 1] : 0);
-    hist[lv] = incl - c;
-    if (tid == 1023) {
-      a.head->n_tiles = min(incl, a.max_tiles);
-      a.head->ok = 1;
+    for (int i = 0; i < PER; ++i) {
+      hist[kPlanLevels - 1 - (tid * PER + i)] = x;
+      x += c[i];
     }
   }
   __syncthreads();
-  // exclusive scan of the sequences' query rows
-  for (int b0 = 0; a.qoff && b0 < a.batch; b0 += 1024) {
-    const int b = b0 + tid;
-    const int c = b < a.batch ? window_pad(a.cu[b + 1] - a.cu[b], a.obs) : 0;
-    int x = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) wsum[warp] = x;
-    __syncthreads();
-    int before = carry;
-    for (int w = 0; w < warp; ++w) before += wsum[w];
-    if (b < a.batch) a.qoff[b] = before + x - c;
-    __syncthreads();
-    if (tid == 1023) carry = before + x;
-    __syncthreads();
-  }
-  if (a.qoff && tid == 0) a.qoff[a.batch] = carry;
-  __syncthreads();  // the offsets are written: each warp reads those of its sequences
-  for (int b = warp; b < a.batch; b += 32) {
+  for (int b = warp; b < a.batch; b += kPlanThreads / 32) {
     PackedTile e;
     e.seq = b;
     e.first = a.cu[b];
     e.n = a.cu[b + 1] - e.first;
-    e.qoff = a.qoff ? a.qoff[b] : 0;
-    e.pad[0] = e.pad[1] = e.pad[2] = 0;
     for (int t = lane; t * 128LL < e.n; t += 32) {
       e.t = t;
       const int at = atomicAdd(&hist[level(e.n, t)], 1);
@@ -208,11 +179,10 @@ struct PackedRopeArgs {
   const void* q;
   const void* k;
   const void* v;
-  const int* cu;
-  const PlanHeader* head;
-  int batch, total_rows, hq, hkv;
+  PlanArgs plan;
+  int hq, hkv;
   int w0, w_pretrained, mode, window;
-  __half* Qo;  // [hq, T, D]; Ql / Kl rows are written only where a sequence has a long-range branch
+  __half* Qo;  // [hq, T, D]; the long-range forms are written only where they are used
   __half* Ql;
   __half* Ko;  // [hkv, T, D]
   __half* Kl;
@@ -224,105 +194,169 @@ struct PackedRopeArgs {
   double omega[64];
 };
 
-// One warp per packed row; lanes as in rope_prepass_kernel (4 groups of 8, a group per head, a lane
-// 8 pairs). Memory bound: it reads q, k, v once and writes the operand forms once.
-template <typename Tin, int D>
-__global__ void __launch_bounds__(256) rope_packed_kernel(const __grid_constant__ PackedRopeArgs a) {
+// Eight values to fp16, and the largest magnitude among all so rounded: a value that fp16 cannot hold rounds to
+// inf, a NaN stays one, and the maximum that keeps NaNs finds either with one instruction for two values.
+__device__ __forceinline__ uint4 to_f16(const float (&x)[8], __half2& top) {
+  uint32_t h[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    h[e] = pack_f16x2(x[2 * e], x[2 * e + 1]);
+    top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __half2*>(&h[e])));
+  }
+  return make_uint4(h[0], h[1], h[2], h[3]);
+}
+__device__ __forceinline__ bool all_finite(__half2 top) {
+  const float2 f = __half22float2(top);
+  return f.x < INFINITY && f.y < INFINITY;  // false for a NaN
+}
+
+// What a CTA's warps need of each of its rows.
+struct RopeRow {
+  int b, p, G;       // sequence (-1: none), position, factor
+  int lng_q, lng_k;  // whether the row's query and key are wanted in the long-range form
+  int row;           // cache row, -1: none
+};
+
+// Eight pairs (x1, x2) turned by the angles of form f: cs holds {cos, sin} of pairs 8 l + 2 e, 8 l + 2 e + 1 at
+// [e][l], so that the lanes of a head read consecutive 16-byte words. Products and sums are fused as the
+// compiler fuses them in rope_prepass_kernel, so that both passes give the same forms bit for bit.
+template <typename V, int LPR>
+__device__ __forceinline__ void turn8(const V& x1, const V& x2, const float4 (&cs)[4][LPR], int l, float (&y1)[8], float (&y2)[8]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float4 t = cs[e][l];
+    const float u0 = x1.get(2 * e), v0 = x2.get(2 * e), u1 = x1.get(2 * e + 1), v1 = x2.get(2 * e + 1);
+    y1[2 * e] = fmaf(u0, t.x, -__fmul_rn(v0, t.y));
+    y2[2 * e] = fmaf(v0, t.x, __fmul_rn(u0, t.y));
+    y1[2 * e + 1] = fmaf(u1, t.z, -__fmul_rn(v1, t.w));
+    y2[2 * e + 1] = fmaf(v1, t.z, __fmul_rn(u1, t.w));
+  }
+}
+
+// A CTA takes ROWS rows (the first CTA makes the tile list instead): it looks them up, evaluates their angles
+// once for all heads (fp64 product and reduction, see angle_cos_sin), then deals (row, four heads) units to its
+// warps, eight lanes a head and eight pairs a lane. A warp keeps UNITS loads in flight, the first ones while the
+// angles are formed. Memory bound: it reads q, k, v once and writes each form once. The long-range forms that no
+// pair uses are left out: of queries in the 128 rows of an attention tile that ends before w0 (no key is that
+// far back), and of keys in a tile that no query of the sequence is w0 past.
+template <typename Tin, int D, int ROWS>
+__global__ void __launch_bounds__(kPlanThreads, sizeof(Tin) == 2 ? 3 : 2) rope_packed_kernel(const __grid_constant__ PackedRopeArgs a) {
   constexpr int P = D / 2;
-  constexpr int NPAIR = 8;
-  constexpr int LANES_PER_ROW = P / NPAIR;
+  constexpr int LPR = P / 8;  // lanes a head
+  constexpr int UNITS = 3;
+  __shared__ RopeRow s_row[ROWS];
+  __shared__ float4 s_cs[ROWS][2][4][LPR];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = blockIdx.x * 8 + warp;
+  const int grp = lane >> 3, l8 = lane & 7, k0 = l8 * 8;
+  const int r0 = static_cast<int>(blockIdx.x - 1) * ROWS;
+  const int heads = a.hq + 2 * a.hkv, per_row = (heads + 3) / 4;
+  const int n_units = min(ROWS, a.plan.total_rows - r0) * per_row;
+  const bool want_v = a.Vb || a.vcache;
+  Vec8<Tin> x1[UNITS], x2[UNITS];
+  auto load = [&](int u, Vec8<Tin>& y1, Vec8<Tin>& y2) {
+    const int rr = u / per_row, hh = u % per_row * 4 + grp;
+    if (u >= n_units || hh >= heads || l8 >= LPR) return;
+    const long long r = r0 + rr;
+    const Tin* src = hh < a.hq           ? static_cast<const Tin*>(a.q) + (r * a.hq + hh) * D
+                     : hh < a.hq + a.hkv ? static_cast<const Tin*>(a.k) + (r * a.hkv + hh - a.hq) * D
+                                         : static_cast<const Tin*>(a.v) + (r * a.hkv + hh - a.hq - a.hkv) * D;
+    if (hh >= a.hq + a.hkv && !want_v) return;
+    y1.load(src + k0);
+    y2.load(src + P + k0);
+  };
   pdl_launch_dependents();
   pdl_wait();
-  if (r >= a.total_rows || !a.head->ok) return;
-  const int b = sequence_of(a.cu, a.batch, r);
-  if (b < 0) return;
-  const int first = a.cu[b], n = a.cu[b + 1] - first, p = r - first;
-  const int G = factor_of(n, a.w_pretrained);
-  const bool lng = !a.window && has_long_pairs(n, G, a.w0);
-  const int grp = lane >> 3, l8 = lane & 7;
-  if (l8 >= LANES_PER_ROW) return;
-  const int k0 = l8 * NPAIR;
-  long long crow = -1;
-  if (a.kcache) {
-    crow = cache_row(a.rows, b, p, r);
-    if (crow < 0 && lane == 0) report_status(kDevIndex, 61);
+  if (blockIdx.x > 0)
+#pragma unroll
+    for (int j = 0; j < UNITS; ++j) load(warp + 8 * j, x1[j], x2[j]);
+  const bool ok = boundaries_ok(a.plan);
+  if (blockIdx.x == 0) {
+    plan_tiles(a.plan, ok);
+    return;
   }
-
-  float co[NPAIR], so[NPAIR], cl[NPAIR], sl[NPAIR];
-#pragma unroll
-  for (int i = 0; i < NPAIR; ++i) {
-    const double w = a.omega[k0 + i];
-    angle_cos_sin(static_cast<double>(p) * w, co[i], so[i]);
-    if (lng) angle_cos_sin(a.mode == 0 ? static_cast<double>(p) * (w / G) : static_cast<double>(p / G) * w, cl[i], sl[i]);
-  }
-  const Tin* qb = static_cast<const Tin*>(a.q);
-  const Tin* kb = static_cast<const Tin*>(a.k);
-  const Tin* vb = static_cast<const Tin*>(a.v);
-  for (int hh = grp; hh < a.hq + a.hkv; hh += 4) {
-    const bool is_q = hh < a.hq;
-    const int h = is_q ? hh : hh - a.hq;
-    const Tin* src = (is_q ? qb + (static_cast<long long>(r) * a.hq + h) * D : kb + (static_cast<long long>(r) * a.hkv + h) * D);
-    Vec8<Tin> x1, x2;
-    x1.load(src + k0);
-    x2.load(src + P + k0);
-    float y1[8], y2[8];
-    bool fin = true;
-#pragma unroll
-    for (int i = 0; i < NPAIR; ++i) {
-      const float u = x1.get(i), w = x2.get(i);
-      y1[i] = u * co[i] - w * so[i];
-      y2[i] = w * co[i] + u * so[i];
-      fin &= f16_ok(y1[i]) & f16_ok(y2[i]);
-    }
-    const long long at = (static_cast<long long>(h) * a.total_rows + r) * D;
-    __half* dst_o = (is_q ? a.Qo : a.Ko) + at;
-    store8_f16(dst_o + k0, y1);
-    store8_f16(dst_o + P + k0, y2);
-    if (!is_q && crow >= 0) {
-      __nv_bfloat16* dc = a.kcache + (crow * a.hkv + h) * D;
-      store8_bf16(dc + k0, y1);
-      store8_bf16(dc + P + k0, y2);
-      if (a.kpos && l8 == 0) a.kpos[static_cast<long long>(h) * a.rows.rows + crow] = p;
-    }
-    if (lng) {
-#pragma unroll
-      for (int i = 0; i < NPAIR; ++i) {
-        const float u = x1.get(i), w = x2.get(i);
-        y1[i] = u * cl[i] - w * sl[i];
-        y2[i] = w * cl[i] + u * sl[i];
-        fin &= f16_ok(y1[i]) & f16_ok(y2[i]);
-      }
-      __half* dst_l = (is_q ? a.Ql : a.Kl) + at;
-      store8_f16(dst_l + k0, y1);
-      store8_f16(dst_l + P + k0, y2);
-    }
-    if (!fin) report_status(kDevRange, 62);
-  }
-  if (a.Vb || crow >= 0) {
-    for (int h = grp; h < a.hkv; h += 4) {
-      const long long off = (static_cast<long long>(r) * a.hkv + h) * D;
-      Vec8<Tin> x1, x2;
-      x1.load(vb + off + k0);
-      x2.load(vb + off + P + k0);
-      float y1[8], y2[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        y1[i] = x1.get(i);
-        y2[i] = x2.get(i);
-      }
-      if (a.Vb) {
-        store8_bf16(a.Vb + off + k0, y1);
-        store8_bf16(a.Vb + off + P + k0, y2);
-      }
-      if (crow >= 0) {
-        __nv_bfloat16* dv = a.vcache + (crow * a.hkv + h) * D;
-        store8_bf16(dv + k0, y1);
-        store8_bf16(dv + P + k0, y2);
+  if (!ok) return;
+  if (threadIdx.x < ROWS) {
+    RopeRow w;
+    const int r = r0 + threadIdx.x;
+    w.b = r < a.plan.total_rows ? sequence_of(a.plan.cu, a.plan.batch, r) : -1;
+    w.row = -1;
+    if (w.b >= 0) {
+      const int first = a.plan.cu[w.b], n = a.plan.cu[w.b + 1] - first;
+      w.p = r - first;
+      w.G = factor_of(n, a.w_pretrained);
+      const bool lng = !a.window && has_long_pairs(n, w.G, a.w0);
+      w.lng_q = lng && (w.p | 127) >= a.w0;
+      w.lng_k = lng && n - 1 - (w.p & ~127) >= a.w0;
+      if (a.kcache) {
+        const long long c = cache_row(a.rows, w.b, w.p, r);
+        if (c < 0) report_status(kDevIndex, 61);
+        w.row = static_cast<int>(c);
       }
     }
+    s_row[threadIdx.x] = w;
   }
+  __syncthreads();
+  for (int i = threadIdx.x; i < ROWS * 2 * P; i += kPlanThreads) {
+    const int rr = i / (2 * P), f = i / P % 2, k = i % P;
+    const RopeRow w = s_row[rr];
+    if (w.b < 0 || (f == 1 && !w.lng_q && !w.lng_k)) continue;
+    const double om = a.omega[k];
+    float c, s;
+    angle_cos_sin(f == 0        ? static_cast<double>(w.p) * om
+                  : a.mode == 0 ? static_cast<double>(w.p) * (om / w.G)
+                                : static_cast<double>(w.p / w.G) * om,
+                  c, s);
+    reinterpret_cast<float2*>(&s_cs[rr][f][k % 8 / 2][k / 8])[k % 2] = make_float2(c, s);
+  }
+  __syncthreads();
+  __half2 top = __float2half2_rn(0.f);
+  for (int u0 = warp; u0 < n_units; u0 += 8 * UNITS) {
+#pragma unroll
+    for (int j = 0; j < UNITS; ++j) {
+      const int u = u0 + 8 * j;
+      const int rr = min(u / per_row, ROWS - 1), hh = u % per_row * 4 + grp;
+      const RopeRow w = s_row[rr];
+      const bool is_q = hh < a.hq, is_v = hh >= a.hq + a.hkv;
+      if (u < n_units && hh < heads && l8 < LPR && w.b >= 0 && (!is_v || want_v)) {
+        const long long r = r0 + rr, crow = w.row;
+        const int h = is_q ? hh : hh - a.hq - (is_v ? a.hkv : 0);
+        float y1[8], y2[8];
+        if (is_v) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            y1[i] = x1[j].get(i);
+            y2[i] = x2[j].get(i);
+          }
+          if (a.Vb) {
+            store8_bf16(a.Vb + (r * a.hkv + h) * D + k0, y1);
+            store8_bf16(a.Vb + (r * a.hkv + h) * D + P + k0, y2);
+          }
+          if (crow >= 0) {
+            store8_bf16(a.vcache + (crow * a.hkv + h) * D + k0, y1);
+            store8_bf16(a.vcache + (crow * a.hkv + h) * D + P + k0, y2);
+          }
+        } else {
+          const long long at = (static_cast<long long>(h) * a.plan.total_rows + r) * D;
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            if (f == 1 && !(is_q ? w.lng_q : w.lng_k)) break;
+            turn8(x1[j], x2[j], s_cs[rr][f], l8, y1, y2);
+            __half* dst = (is_q ? (f == 0 ? a.Qo : a.Ql) : (f == 0 ? a.Ko : a.Kl)) + at;
+            *reinterpret_cast<uint4*>(dst + k0) = to_f16(y1, top);
+            *reinterpret_cast<uint4*>(dst + P + k0) = to_f16(y2, top);
+            if (f == 0 && !is_q && crow >= 0) {
+              __nv_bfloat16* dc = a.kcache + (crow * a.hkv + h) * D;
+              store8_bf16(dc + k0, y1);
+              store8_bf16(dc + P + k0, y2);
+              if (a.kpos && l8 == 0) a.kpos[static_cast<long long>(h) * a.rows.rows + crow] = w.p;
+            }
+          }
+        }
+      }
+      load(u + 8 * UNITS, x1[j], x2[j]);
+    }
+  }
+  if (!all_finite(top)) report_status(kDevRange, 62);
 }
 
 // What the attention kernels' packed form adds to their arguments: the tile list and boundaries.

@@ -34,19 +34,18 @@ bf_status_t check_packed(int32_t dtype, int32_t batch, int32_t total_rows, int32
   return BF_OK;
 }
 
-cudaError_t launch_plan(const int32_t* cu, int batch, int total_rows, int max_len, int obs, bf::PlanHeader* head,
-                        bf::PackedTile* tiles, int max_tiles, int* qoff, cudaStream_t st) {
+bf::PlanArgs make_plan(const int32_t* cu, int batch, int total_rows, int max_len, int obs, uint8_t* ws, size_t tiles,
+                       int max_tiles) {
   bf::PlanArgs a{};
   a.cu = cu;
   a.batch = batch;
   a.total_rows = total_rows;
   a.max_len = max_len;
   a.obs = obs;
-  a.head = head;
-  a.tiles = tiles;
+  a.head = reinterpret_cast<bf::PlanHeader*>(ws);
+  a.tiles = reinterpret_cast<bf::PackedTile*>(ws + tiles);
   a.max_tiles = max_tiles;
-  a.qoff = qoff;
-  return launch_pdl(bf::packed_plan_kernel, dim3(1), dim3(1024), 0, st, a);
+  return a;
 }
 
 // ------------------------------------------------------------------ packed prefill
@@ -92,17 +91,16 @@ bool make_value_map(CUtensorMap* map, const void* base, int64_t rows, int hkv, i
                            static_cast<cuuint64_t>(rows) * hkv * D * 2};
   cuuint32_t box[4] = {64, 1, 128, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
 }
 
 template <typename Args>
 cudaError_t launch_packed(void (*kern)(const Args), int64_t ctas, int threads, int smem, const Args& args, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(ctas), threads, smem, st>>>(args);
-  return cudaGetLastError();
+  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(threads), smem, st, args);
 }
 
 // The ping-pong kernel (even groups) and the single-tile kernel (odd ones), for either head size.
@@ -118,6 +116,15 @@ template <int D>
 cudaError_t launch_packed_tc(bool bif, const bf::TcArgs& a, int64_t ctas, cudaStream_t st) {
   auto kern = bif ? bf::attn_tc_kernel<true, true, D> : bf::attn_tc_kernel<false, true, D>;
   return launch_packed(kern, ctas, bf::tc::NTHREADS, bf::attn_tc_smem_bytes(), a, st);
+}
+
+// Few rows are spread over more CTAs: two a CTA up to 2048 rows, else eight.
+template <typename Tin, int D>
+cudaError_t launch_rope_packed(const bf::PackedRopeArgs& a, cudaStream_t st) {
+  const int rows = a.plan.total_rows <= 2048 ? 2 : 8;
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.plan.total_rows) + rows - 1) / rows + 1));
+  return rows == 2 ? launch_pdl(bf::rope_packed_kernel<Tin, D, 2>, grid, dim3(bf::kPlanThreads), 0, st, a)
+                   : launch_pdl(bf::rope_packed_kernel<Tin, D, 8>, grid, dim3(bf::kPlanThreads), 0, st, a);
 }
 
 bf_status_t prefill_packed_impl(const void* q, const void* k, const void* v, int32_t dtype, int32_t total_rows,
@@ -152,23 +159,14 @@ bf_status_t prefill_packed_impl(const void* q, const void* k, const void* v, int
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const int D = p->head_dim;
-  auto* head = reinterpret_cast<bf::PlanHeader*>(ws);
-  auto* tiles = reinterpret_cast<bf::PackedTile*>(ws + lay.tiles);
 
-  // 1. the tile list
-  if (launch_plan(cu_seqlens, batch, total_rows, max_len, 0, head, tiles, max_tiles, nullptr, st) != cudaSuccess)
-    return BF_ERR_CUDA;
-
-  // 2. the RoPE pass: operand forms and cache rows
+  // 1. the RoPE pass: operand forms and cache rows; its first CTA makes the tile list
   const Rope rope = make_rope(p->rope_theta, D, 1);
   bf::PackedRopeArgs pa{};
   pa.q = q;
   pa.k = k;
   pa.v = v;
-  pa.cu = cu_seqlens;
-  pa.head = head;
-  pa.batch = batch;
-  pa.total_rows = total_rows;
+  pa.plan = make_plan(cu_seqlens, batch, total_rows, max_len, 0, ws, lay.tiles, max_tiles);
   pa.hq = p->hq;
   pa.hkv = p->hkv;
   pa.w0 = p->w0;
@@ -185,23 +183,20 @@ bf_status_t prefill_packed_impl(const void* q, const void* k, const void* v, int
   pa.kpos = kpos;
   pa.rows = rows;
   std::memcpy(pa.omega, rope.omega, sizeof(pa.omega));
-  const dim3 pgrid(static_cast<unsigned>((static_cast<int64_t>(total_rows) + 7) / 8));
   cudaError_t e;
   if (dtype == BF_DTYPE_BF16)
-    e = D == 128 ? launch_pdl(bf::rope_packed_kernel<bf16, 128>, pgrid, dim3(256), 0, st, pa)
-                 : launch_pdl(bf::rope_packed_kernel<bf16, 64>, pgrid, dim3(256), 0, st, pa);
+    e = D == 128 ? launch_rope_packed<bf16, 128>(pa, st) : launch_rope_packed<bf16, 64>(pa, st);
   else
-    e = D == 128 ? launch_pdl(bf::rope_packed_kernel<float, 128>, pgrid, dim3(256), 0, st, pa)
-                 : launch_pdl(bf::rope_packed_kernel<float, 64>, pgrid, dim3(256), 0, st, pa);
+    e = D == 128 ? launch_rope_packed<float, 128>(pa, st) : launch_rope_packed<float, 64>(pa, st);
   if (e != cudaSuccess) return BF_ERR_CUDA;
 
-  // 3. attention. The two-branch kernel only when some sequence may be longer than both the
+  // 2. attention. The two-branch kernel only when some sequence may be longer than both the
   // pretrained window and w0; one without long-range pairs runs it with every pair local
   const void* vsrc = dtype == BF_DTYPE_FP32 ? static_cast<const void*>(ws + lay.vb) : v;
   const bool bif = !window && factor(max_len, p->w_pretrained) > 1 && p->w0 < max_len;
   bf::PackedTiles pt{};
-  pt.head = head;
-  pt.tiles = tiles;
+  pt.head = pa.plan.head;
+  pt.tiles = pa.plan.tiles;
   pt.max_tiles = max_tiles;
   pt.total_rows = total_rows;
   pt.w_pretrained = p->w_pretrained;
@@ -467,18 +462,20 @@ bf_status_t cache_evict_impl(void* kcache, void* vcache, int32_t* kpos, float* k
 
 // ------------------------------------------------------------------ attention weight of keys
 struct WeightLayout {
-  size_t tiles, qoff, forms, form_bytes, nl, total;
-  int64_t max_tiles, rows;  // rows: of the query forms, at most
+  size_t tiles, forms, form_bytes, nl, total;
+  int64_t max_tiles, rows;  // rows: queries of the forms
+  int window_pitch;         // of them a sequence, 0: as many as it has rows
 };
 
 WeightLayout weight_layout(int batch, int T, int obs, const bf_params_t* p) {
   WeightLayout w{};
   w.max_tiles = packed_max_tiles(T, batch);
-  w.rows = std::min<int64_t>(static_cast<int64_t>(T) + 3LL * batch, (static_cast<int64_t>(obs) + 3) * batch);
-  w.rows = (w.rows + 3) / 4 * 4;
+  // a window of obs queries a sequence, or (when that is more) the rows of the sequences themselves
+  const int64_t pitch = (static_cast<int64_t>(obs) + 3) / 4 * 4, packed = (static_cast<int64_t>(T) + 3LL * batch + 7) / 4 * 4;
+  w.window_pitch = pitch * batch <= packed ? static_cast<int>(pitch) : 0;
+  w.rows = w.window_pitch ? pitch * batch : packed;
   w.tiles = 256;
-  w.qoff = w.tiles + align256(static_cast<size_t>(w.max_tiles) * sizeof(bf::PackedTile));
-  w.forms = w.qoff + align256((static_cast<size_t>(batch) + 1) * 4);
+  w.forms = w.tiles + align256(static_cast<size_t>(w.max_tiles) * sizeof(bf::PackedTile));
   w.form_bytes = align256(static_cast<size_t>(w.rows) * p->hq * p->head_dim * 2);
   w.nl = w.forms + 4 * w.form_bytes;
   w.total = w.nl + align256((static_cast<size_t>(w.rows) * (p->hq / p->hkv) + 128) * p->hkv * 4);
@@ -491,15 +488,15 @@ cudaError_t launch_weights_qt(const bf::WeightArgs& a, cudaStream_t st) {
   auto kern = bf::key_weights_kernel<Tin, D, QT>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(a.max_tiles) * a.hkv), dim3(bf::kw::NTHREADS), smem, st, a);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(a.plan.max_tiles) * a.hkv), dim3(bf::kw::NTHREADS), smem, st, a);
 }
 
 template <typename Tin, int D>
 cudaError_t launch_weights(const bf::WeightArgs& a, int qt, cudaStream_t st) {
-  // all heads in one warp from 4096 queries on (512 CTAs)
-  const int y = a.form_rows >= 4096 ? 1 : (a.hq + 3) / 4;
+  const int64_t units = a.window_pitch ? a.form_rows : a.plan.total_rows;
   const cudaError_t e = launch_pdl(bf::weights_query_kernel<Tin, D>,
-                                   dim3(static_cast<unsigned>((a.form_rows + 7LL) / 8), y), dim3(256), 0, st, a);
+                                   dim3(static_cast<unsigned>((units + bf::kw::QROWS - 1) / bf::kw::QROWS + 1)),
+                                   dim3(bf::kPlanThreads), 0, st, a);
   if (e != cudaSuccess) return e;
   return qt == 64 ? launch_weights_qt<Tin, D, 64>(a, st) : launch_weights_qt<Tin, D, 128>(a, st);
 }
@@ -533,31 +530,19 @@ bf_status_t key_weights_impl(const void* q, const void* k, int32_t dtype, const 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int D = p->head_dim;
-  auto* head = reinterpret_cast<bf::PlanHeader*>(ws);
-  auto* tiles = reinterpret_cast<bf::PackedTile*>(ws + lay.tiles);
-  int* qoff = reinterpret_cast<int*>(ws + lay.qoff);
   CUtensorMap* maps[4] = {&a.qo_hi, &a.qo_lo, &a.ql_hi, &a.ql_lo};
   for (int i = 0; i < 4; ++i) {
     a.forms[i] = reinterpret_cast<__half*>(ws + lay.forms + i * lay.form_bytes);
     if (!make_form_map(maps[i], a.forms[i], lay.rows * g, p->hkv, D, qt)) return BF_ERR_CUDA;
   }
-  if (launch_plan(cu_seqlens, batch, total_rows, max_len, obs, head, tiles, static_cast<int>(lay.max_tiles), qoff, st) !=
-      cudaSuccess)
-    return BF_ERR_CUDA;
   const Rope rope = make_rope(p->rope_theta, D, 1);
   a.q = q;
   a.k = k;
   a.lse = lse;
-  a.cu = cu_seqlens;
-  a.head = head;
-  a.tiles = tiles;
-  a.qoff = qoff;
-  a.batch = batch;
-  a.total_rows = total_rows;
+  a.plan = make_plan(cu_seqlens, batch, total_rows, max_len, obs, ws, lay.tiles, static_cast<int>(lay.max_tiles));
+  a.window_pitch = lay.window_pitch;
   a.hq = p->hq;
   a.hkv = p->hkv;
-  a.max_tiles = static_cast<int>(lay.max_tiles);
-  a.obs = obs;
   a.w0 = p->w0;
   a.w_pretrained = p->w_pretrained;
   a.mode = p->mode;

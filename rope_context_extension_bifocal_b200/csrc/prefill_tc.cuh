@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(tc::NTHREADS, 1) attn_tc_kernel(const __grid_c
   int h, b, i0, L = a.L, row0 = 0, pitch = a.L, w0 = a.w0;
   if (PACKED) {
     const int rank = static_cast<int>(blockIdx.x) / a.hq;
+    pdl_wait();  // the tile list and the operand forms are the previous kernel's
     const PackedTile tile = a.packed.tiles[rank];
     if (rank >= a.packed.head->n_tiles) return;
     h = static_cast<int>(blockIdx.x) % a.hq;

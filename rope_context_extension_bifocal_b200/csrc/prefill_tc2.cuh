@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __gri
     const int ppk = pairs / a.hkv;
     const int idx = static_cast<int>(blockIdx.x);
     const int rank = idx / ppk % a.packed.max_tiles;
+    pdl_wait();  // the tile list and the operand forms are the previous kernel's
     const PackedTile tile = a.packed.tiles[rank];
     if (rank >= a.packed.head->n_tiles) return;
     hp = idx / (ppk * a.packed.max_tiles) * ppk + idx % ppk;
