@@ -20,6 +20,13 @@ bf_status_t make_cache_rows(int64_t cache_rows, int32_t page_size, const int32_t
   return BF_OK;
 }
 
+// log2 of a page size, -1 when it is not a power of two (the kernels then divide).
+int page_shift(int page_size) {
+  for (int i = 0; i < 31; ++i)
+    if (page_size == 1 << i) return i;
+  return -1;
+}
+
 int64_t packed_max_tiles(int64_t total_rows, int64_t batch) {
   return total_rows / 128 + std::min(batch, total_rows);
 }
@@ -320,9 +327,7 @@ bf_status_t decode_kept_impl(const void* q, const void* k_new, const void* v_new
   if (!workspace || !aligned(workspace, 256) || ws_bytes < lay.total) return BF_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const Rope rope = make_rope(p->rope_theta, p->head_dim, 1);
-  a.page_shift = -1;
-  for (int i = 0; i < 31; ++i)
-    if (page_size == 1 << i) a.page_shift = i;
+  a.page_shift = page_shift(page_size);
   a.q = static_cast<const bf16*>(q);
   a.k_new = static_cast<const bf16*>(k_new);
   a.v_new = static_cast<const bf16*>(v_new);
@@ -360,7 +365,7 @@ struct EvictLayout {
   int pitch;
 };
 
-EvictLayout evict_layout(int batch, int hkv, int max_len, int budget, bool in_place) {
+EvictLayout evict_layout(int batch, int hkv, int max_len, int budget) {
   EvictLayout w{};
   const size_t segs = static_cast<size_t>(batch) * hkv;
   w.pitch = std::min(max_len, budget);
@@ -368,7 +373,7 @@ EvictLayout evict_layout(int batch, int hkv, int max_len, int budget, bool in_pl
   w.lens = align256(segs * 4);
   w.from = w.lens + align256(static_cast<size_t>(batch) * 4);
   w.to = w.from + list;
-  w.total = w.to + (in_place ? list : 0);
+  w.total = w.to + list;
   return w;
 }
 
@@ -398,7 +403,7 @@ bf_status_t cache_evict_impl(void* kcache, void* vcache, int32_t* kpos, float* k
   if (static_cast<int64_t>(max_pages) * page_size < max_len) return BF_ERR_INVALID;
   a.in_place = dst_block_table ? 0 : 1;
   a.dst = a.src;
-  const EvictLayout lay = evict_layout(batch, hkv, max_len, budget, a.in_place != 0);
+  const EvictLayout lay = evict_layout(batch, hkv, max_len, budget);
   if (dst_block_table) {
     s = make_cache_rows(cache_rows, page_size, dst_block_table, dst_max_pages, &a.dst);
     if (s != BF_OK) return s;
@@ -421,10 +426,12 @@ bf_status_t cache_evict_impl(void* kcache, void* vcache, int32_t* kpos, float* k
   a.moves = reinterpret_cast<int*>(ws);
   a.lens = reinterpret_cast<int*>(ws + lay.lens);
   a.from = reinterpret_cast<int*>(ws + lay.from);
-  a.to = reinterpret_cast<int*>(ws + (a.in_place ? lay.to : lay.from));
+  a.to = reinterpret_cast<int*>(ws + lay.to);
   a.pitch = lay.pitch;
-  // a CTA for up to 4096 slots, a cluster of up to 8 for more
-  const int size = max_len <= 4096 ? 1 : max_len <= 8192 ? 2 : max_len <= 16384 ? 4 : 8;
+  a.page_shift = page_shift(page_size);
+  // a CTA for every CTA_SLOTS slots, in clusters of up to 8
+  int size = 1;
+  while (size < 8 && static_cast<int64_t>(size) * bf::ev::CTA_SLOTS < max_len) size *= 2;
   // the slots of a CTA as the kernel divides them
   const int64_t per_cta = ((static_cast<int64_t>(max_len) + size * bf::ev::WARPS - 1) / (size * bf::ev::WARPS) + 31) / 32 *
                           32 * bf::ev::WARPS;
@@ -450,10 +457,9 @@ bf_status_t cache_evict_impl(void* kcache, void* vcache, int32_t* kpos, float* k
   cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, bf::evict_select_kernel, a);
   if (e != cudaSuccess) return BF_ERR_CUDA;
-  // rows to move: a warp per 4 (D = 128) or 8 rows, about 2048 CTAs at most
+  // rows to move: eight a warp, 64 a CTA; at most about 16384 CTAs, which then take several turns
   const int64_t segs = static_cast<int64_t>(batch) * hkv;
-  const int rows_per_cta = 8 * 4 * (head_dim == 128 ? 1 : 2);
-  const int64_t x = std::max<int64_t>(1, std::min<int64_t>((lay.pitch + rows_per_cta - 1) / rows_per_cta, (2048 + segs - 1) / segs));
+  const int64_t x = std::max<int64_t>(1, std::min<int64_t>((lay.pitch + 63) / 64, (16384 + segs - 1) / segs));
   const dim3 grid(static_cast<unsigned>(x), hkv, batch);
   e = head_dim == 128 ? launch_pdl(bf::evict_move_kernel<128>, grid, dim3(256), 0, st, a)
                       : launch_pdl(bf::evict_move_kernel<64>, grid, dim3(256), 0, st, a);
@@ -597,7 +603,7 @@ bf_status_t bifocal_decode_kept(const void* q, const void* k_new, const void* v_
 
 size_t bifocal_cache_evict_workspace_size(int32_t batch, int32_t hkv, int32_t max_len, int32_t budget) {
   if (check_evict(batch, hkv, 64, max_len, budget) != BF_OK) return 0;
-  return evict_layout(batch, hkv, max_len, budget, true).total;
+  return evict_layout(batch, hkv, max_len, budget).total;
 }
 
 bf_status_t bifocal_cache_evict(void* kcache, void* vcache, int32_t* kpos, float* kweight, int64_t cache_rows,
