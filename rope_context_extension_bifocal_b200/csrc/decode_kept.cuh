@@ -37,6 +37,8 @@ constexpr int MAX_G = 8;    // query heads per kv head (max)
 }  // namespace kept
 
 struct KeptArgs {
+  CUtensorMap k_map, v_map;    // cache rows [rows][hkv][D], box (D, 1, a stage's slots); with boxes
+  int boxes;                   // pages hold whole stages
   const __nv_bfloat16* q;      // [B, hq, D] raw
   const __nv_bfloat16* k_new;  // [B, hkv, D] raw
   const __nv_bfloat16* v_new;
@@ -100,6 +102,7 @@ __global__ void __launch_bounds__(kept::WARPS * 32, GP <= 4 ? 4 : 2) decode_kept
   static_assert(CH * D * 4 == STAGE_BYTES, "a stage holds the keys and values of CH slots");
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ __align__(16) float2 sp[WARPS][KPW][NV];  // probabilities, twice each (packed operands)
+  __shared__ uint64_t s_full[WARPS * STAGES];          // a warp's stages have landed
   __shared__ float sm[WARPS][GP], sl[WARPS][GP];
 
   pdl_launch_dependents();
@@ -134,32 +137,58 @@ __global__ void __launch_bounds__(kept::WARPS * 32, GP <= 4 ? 4 : 2) decode_kept
       }
     }
   };
-  // One stage: the K and V rows of slots CH sub .. of the block whose rows are `row`, 16 bytes a lane. A copy of
-  // 32 lanes is one slot (D = 128: 16 lanes its key, 16 its value) or two.
+  // One stage: the K and V rows of slots CH sub .. of the block whose rows are `row`, as one box each where pages
+  // hold whole stages (two instructions of one lane), else row by row (a lane each). Rows that are no slot of the
+  // range are whatever is there; they are zeroed when the stage is used.
   uint8_t* stages = smem + warp * STAGES * STAGE_BYTES;
-  const uint32_t st0 = smem_u32(stages);
-  const int c_lane = lane % (D / 4), c_slot = lane / (D / 4);  // lane of a slot's D / 4 lanes, slot of the copy
-  const bool c_is_v = c_lane >= D / 8;
-  const __nv_bfloat16* c_src = (c_is_v ? a.vcache : a.kcache) + static_cast<long long>(kvh) * D + (c_lane % (D / 8)) * 8;
-  const long long c_stride = static_cast<long long>(a.hkv) * D;
-  constexpr int SPC = 128 / D;  // slots a copy
+  uint64_t* full = s_full + warp * STAGES;
   auto fill = [&](int stage, int row, int sub) {
-#pragma unroll
-    for (int i = 0; i < CH / SPC; ++i) {
-      const int r = __shfl_sync(0xffffffffu, row, sub * CH + i * SPC + c_slot);
-      cp_async_16(st0 + stage * STAGE_BYTES + i * 512 + lane * 16, c_src + (r >= 0 ? r * c_stride : 0), r >= 0);
+    uint8_t* dst = stages + stage * STAGE_BYTES;
+    if (a.boxes) {
+      const int r = __shfl_sync(0xffffffffu, row, sub * CH);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
+        tma_load_3d(dst, &a.k_map, &full[stage], 0, kvh, max(r, 0));
+        tma_load_3d(dst + STAGE_BYTES / 2, &a.v_map, &full[stage], 0, kvh, max(r, 0));
+      }
+    } else {
+      const int r = __shfl_sync(0xffffffffu, row, sub * CH + lane % CH);
+      if (lane == 0) mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
+      __syncwarp();
+      if (lane < 2 * CH) {
+        const __nv_bfloat16* src = (lane < CH ? a.kcache : a.vcache) + (static_cast<long long>(max(r, 0)) * a.hkv + kvh) * D;
+        asm volatile(
+            "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                smem_u32(dst + lane * (2 * D))),
+            "l"(src), "r"(2 * D), "r"(smem_u32(&full[stage]))
+            : "memory");
+      }
     }
   };
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < WARPS * STAGES; ++i) mbar_init(&s_full[i], 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
 
   int row, pos, nrow, npos;
   int base = s_beg + warp * 32;
   lookup(base, row, pos);
   lookup(base + WARPS * 32, nrow, npos);
-  // two stages ahead of the one in use
+  // two stages ahead of the one in use; a stage past the range is not filled
+  uint32_t used = 0, par = 0;  // per stage: filled at all, parity of its fills
+  auto fill_ahead = [&](int stage, int at, int r, int sub) {
+    if (at >= s_end) return;
+    fill(stage, r, sub);
+    used |= 1u << stage;
+    par ^= 1u << stage;
+  };
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) {
-    if (i < SUB) fill(i, row, i); else fill(i, nrow, i - SUB);
-    cp_async_commit();
+    if (i < SUB)
+      fill_ahead(i, base + i * CH, row, i);
+    else
+      fill_ahead(i, base + WARPS * 32 + (i - SUB) * CH, nrow, i - SUB);
   }
 
   // the query heads' rows under R_l(now) (R_o when nothing is long-range), in the log2 domain, and
@@ -216,37 +245,39 @@ __global__ void __launch_bounds__(kept::WARPS * 32, GP <= 4 ? 4 : 2) decode_kept
   float* score_at = a.scores ? a.scores + (static_cast<long long>(b) * a.hq + kvh * g) * a.pitch : nullptr;
 
   int stage = 0;
-  for (; base < s_end; base += WARPS * 32) {
+  uint32_t phase = 0;  // parity of the next wait on each stage
+  bool ok = true;
+  for (; base < s_end && ok; base += WARPS * 32) {
     const bool is_local = seq.now - pos < a.w0;
     const int mult = is_local ? m_now : far_multiple(pos, seq.G, a.mode);
-    const unsigned local_mask = __ballot_sync(0xffffffffu, is_local);
+    const unsigned local_mask = __ballot_sync(0xffffffffu, is_local), row_mask = __ballot_sync(0xffffffffu, row >= 0);
 #pragma unroll 1
     for (int sub = 0; sub < SUB; ++sub) {
       const int sbase = base + sub * CH;
-      if (sbase >= s_end) {  // warp-uniform: the rest of the last block
-        cp_async_commit();
-        stage = stage == STAGES - 1 ? 0 : stage + 1;
-        continue;
-      }
+      if (sbase >= s_end) break;  // warp-uniform: the rest of the last block
       // two stages on: this block's, or the next one's first
       {
         const int ahead = sub + STAGES - 1, to = stage == 0 ? STAGES - 1 : stage - 1;
-        fill(to, ahead < SUB ? row : nrow, ahead % SUB);
-        cp_async_commit();
+        if (ahead < SUB)
+          fill_ahead(to, base + ahead * CH, row, ahead);
+        else
+          fill_ahead(to, base + WARPS * 32 + (ahead - SUB) * CH, nrow, ahead - SUB);
       }
-      cp_async_wait<STAGES - 1>();
-      __syncwarp();
-      const uint8_t* st = stages + stage * STAGE_BYTES;
-      // scores: this lane's share of each (key, head), then the sum over the key's lanes
-      float val[NV];
-#pragma unroll
-      for (int n = 0; n < NK; ++n) {
-        const int i = n * KPW + kg;
-        uint8_t* kr = const_cast<uint8_t*>(st) + i * (D * 4);
-        uint2 kx = *reinterpret_cast<const uint2*>(kr + ll * 8), ky = *reinterpret_cast<const uint2*>(kr + D + ll * 8);
-        if (sbase + i == seq.n - 1) {
-          // the new token: its key rotated and rounded to the cache's bf16; key, value and position are
-          // appended, and used from here on as the cache holds them
+      ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], (phase >> stage) & 1u, 72));
+      if (!ok) break;
+      phase ^= 1u << stage;
+      uint8_t* st = stages + stage * STAGE_BYTES;
+      const unsigned rows_here = (row_mask >> (sub * CH)) & ((1u << CH) - 1u);
+      const bool append = sbase + CH >= seq.n;
+      if (rows_here != (1u << CH) - 1u || append) {
+        // Rare: rows past the range or of a bad page are zeroed, and the new token's row is written: its key
+        // rotated and rounded to the cache's bf16, so that this step uses it as every later one will.
+        for (int i = 0; i < CH; ++i)
+          if (!((rows_here >> i) & 1u) && lane < 2 * LPK)
+            *reinterpret_cast<uint4*>(st + (lane < LPK ? 0 : STAGE_BYTES / 2) + i * (2 * D) + (lane % LPK) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        __syncwarp();
+        const int i = seq.n - 1 - sbase;
+        if (i >= 0 && i < CH && lane < LPK) {
           const long long src = (static_cast<long long>(b) * a.hkv + kvh) * D;
           const uint2 u = *reinterpret_cast<const uint2*>(a.k_new + src + 4 * ll);
           const uint2 w = *reinterpret_cast<const uint2*>(a.k_new + src + P + 4 * ll);
@@ -260,10 +291,12 @@ __global__ void __launch_bounds__(kept::WARPS * 32, GP <= 4 ? 4 : 2) decode_kept
             x[e] = xr[e] * c - yr[e] * s;
             y[e] = yr[e] * c + xr[e] * s;
           }
-          kx = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-          ky = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+          const uint2 kx = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+          const uint2 ky = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
           const uint4 v = *reinterpret_cast<const uint4*>(a.v_new + src + 8 * ll);
-          *reinterpret_cast<uint4*>(kr + 2 * D + ll * 16) = v;  // read back below by this lane alone
+          *reinterpret_cast<uint2*>(st + i * (2 * D) + ll * 8) = kx;
+          *reinterpret_cast<uint2*>(st + i * (2 * D) + D + ll * 8) = ky;
+          *reinterpret_cast<uint4*>(st + STAGE_BYTES / 2 + i * (2 * D) + ll * 16) = v;
           const int page = (seq.n - 1) / a.rows.page_size, pg = trow[page];
           if (pg >= 0 && pg < a.rows.pool_pages) {
             const long long r = static_cast<long long>(pg) * a.rows.page_size + (seq.n - 1 - page * a.rows.page_size);
@@ -274,6 +307,16 @@ __global__ void __launch_bounds__(kept::WARPS * 32, GP <= 4 ? 4 : 2) decode_kept
             if (ll == 0) a.kpos[static_cast<long long>(kvh) * a.rows.rows + r] = seq.now;
           }
         }
+        fence_proxy_async_smem();  // before the copy that will overwrite the stage
+        __syncwarp();
+      }
+      // scores: this lane's share of each (key, head), then the sum over the key's lanes
+      float val[NV];
+#pragma unroll
+      for (int n = 0; n < NK; ++n) {
+        const int i = n * KPW + kg;
+        const uint2 kx = *reinterpret_cast<const uint2*>(st + i * (2 * D) + ll * 8);
+        const uint2 ky = *reinterpret_cast<const uint2*>(st + i * (2 * D) + D + ll * 8);
         uint64_t x0 = bf16x2_to_f2(kx.x), x1 = bf16x2_to_f2(kx.y), y0 = bf16x2_to_f2(ky.x), y1 = bf16x2_to_f2(ky.y);
         if (seq.rot) {
           const int m = __shfl_sync(0xffffffffu, mult, sub * CH + i);
@@ -348,11 +391,21 @@ __global__ void __launch_bounds__(kept::WARPS * 32, GP <= 4 ? 4 : 2) decode_kept
       __syncwarp();
 #pragma unroll
       for (int n = 0; n < NK; ++n) {
-        const uint4 v = *reinterpret_cast<const uint4*>(st + (n * KPW + kg) * (D * 4) + 2 * D + ll * 16);
+        const uint4 v = *reinterpret_cast<const uint4*>(st + STAGE_BYTES / 2 + (n * KPW + kg) * (2 * D) + ll * 16);
         const uint64_t v0 = bf16x2_to_f2(v.x), v1 = bf16x2_to_f2(v.y), v2 = bf16x2_to_f2(v.z), v3 = bf16x2_to_f2(v.w);
+        uint64_t pp[GP];
+        if (GP == 1)
+          pp[0] = *reinterpret_cast<const uint64_t*>(&sp[warp][kg][n]);
+        else
+#pragma unroll
+          for (int h = 0; h < GP; h += 2) {
+            const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(&sp[warp][kg][n * GP + h]);
+            pp[h] = t.x;
+            pp[h + 1 < GP ? h + 1 : h] = t.y;
+          }
 #pragma unroll
         for (int h = 0; h < GP; ++h) {
-          const uint64_t p2 = *reinterpret_cast<const uint64_t*>(&sp[warp][kg][n * GP + h]);
+          const uint64_t p2 = pp[h];
           o2[h][0] = f2_fma(p2, v0, o2[h][0]);
           o2[h][1] = f2_fma(p2, v1, o2[h][1]);
           o2[h][2] = f2_fma(p2, v2, o2[h][2]);
@@ -366,8 +419,12 @@ __global__ void __launch_bounds__(kept::WARPS * 32, GP <= 4 ? 4 : 2) decode_kept
     pos = npos;
     lookup(base + 2 * WARPS * 32, nrow, npos);
   }
-  cp_async_wait<0>();
-  __syncthreads();  // every warp is done with its stages: the merge reuses them
+  // every copy issued has landed (only an expired wait leaves any), and every warp is done with its stages: the
+  // merge reuses them
+  if (!ok)
+    for (int i = 0; i < STAGES; ++i)
+      if (used & (1u << i)) mbar_wait(&full[i], ((par >> i) & 1u) ^ 1u, 73);
+  __syncthreads();
   float (*so)[GP][D] = reinterpret_cast<float(*)[GP][D]>(smem);
 
   // merge: lane groups by shuffles, warps through shared memory in a fixed order

@@ -257,11 +257,11 @@ struct KeptLayout {
 };
 
 // Ranges of slots: about 1024 CTAs in all (seven of 128 threads on each SM) as long as a range keeps 64
-// slots, and never more than 1024 slots in one, so that a batch of unequal lengths fills the GPU evenly.
+// slots, and never more than 512 slots in one, so that a batch of unequal lengths fills the GPU evenly.
 KeptLayout kept_layout(int batch, int max_len, bool accumulate, const bf_params_t* p) {
   KeptLayout w{};
   const int64_t segs = static_cast<int64_t>(batch) * p->hkv;
-  int64_t n = std::max<int64_t>((1024 + segs - 1) / segs, (static_cast<int64_t>(max_len) + 1023) / 1024);
+  int64_t n = std::max<int64_t>((1024 + segs - 1) / segs, (static_cast<int64_t>(max_len) + 511) / 512);
   n = std::min<int64_t>(n, (static_cast<int64_t>(max_len) + 63) / 64);
   int64_t len = (max_len + n - 1) / n;
   len = (len + 63) / 64 * 64;
@@ -282,6 +282,19 @@ bf_status_t check_kept(int32_t batch, int32_t max_len, const bf_params_t* p) {
   if ((p->flags & BF_FLAG_WINDOW) && p->w0 < 1) return BF_ERR_INVALID;
   if (p->hq / p->hkv > bf::kept::MAX_G || batch > 65535 || p->hkv > 65535) return BF_ERR_UNSUPPORTED;
   return BF_OK;
+}
+
+// Cache rows [rows][hkv][D] bf16, a box of one stage's slots of one head.
+bool make_slot_map(CUtensorMap* map, const void* base, int64_t rows, int hkv, int D) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(hkv), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(hkv) * D * 2};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(D), 1, static_cast<cuuint32_t>(bf::kept::STAGE_BYTES / (4 * D))};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D, int GP>
@@ -319,7 +332,8 @@ bf_status_t decode_kept_impl(const void* q, const void* k_new, const void* v_new
       !aligned(kpos, 4) || !aligned(seq_lens, 4) || !aligned(positions, 4) || !aligned(out, 16) ||
       (kweight && !aligned(kweight, 4)) || (lse && !aligned(lse, 4)))
     return BF_ERR_INVALID;
-  bf::KeptArgs a{};
+  bf::KeptArgs a;
+  std::memset(&a, 0, sizeof(a));
   s = make_cache_rows(cache_rows, page_size, block_table, max_pages, &a.rows);
   if (s != BF_OK) return s;
   if (static_cast<int64_t>(max_pages) * page_size < max_len) return BF_ERR_INVALID;
@@ -328,6 +342,11 @@ bf_status_t decode_kept_impl(const void* q, const void* k_new, const void* v_new
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const Rope rope = make_rope(p->rope_theta, p->head_dim, 1);
   a.page_shift = page_shift(page_size);
+  // a stage's slots share a page, and are one box of the pool, where pages hold whole stages
+  a.boxes = page_size % (bf::kept::STAGE_BYTES / (4 * p->head_dim)) == 0 ? 1 : 0;
+  if (a.boxes && (!make_slot_map(&a.k_map, kcache, cache_rows, p->hkv, p->head_dim) ||
+                  !make_slot_map(&a.v_map, vcache, cache_rows, p->hkv, p->head_dim)))
+    return BF_ERR_CUDA;
   a.q = static_cast<const bf16*>(q);
   a.k_new = static_cast<const bf16*>(k_new);
   a.v_new = static_cast<const bf16*>(v_new);
