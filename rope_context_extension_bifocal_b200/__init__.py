@@ -394,18 +394,28 @@ def _operands(where: str, *tensors):
     for name, t, shape, dtype in tensors:
         if t is None:
             continue
-        if not t.is_cuda or not t.is_contiguous():
+        at = t.device
+        if at != device:
+            if device is not None:
+                raise BifocalError(1, f"{where}: {name} is on {at}, other tensors on {device}")
+            if at.type != "cuda":
+                raise BifocalError(1, f"{where}: {name} must be a contiguous CUDA tensor")
+            device = at
+        if not t.is_contiguous():
             raise BifocalError(1, f"{where}: {name} must be a contiguous CUDA tensor")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise BifocalError(1, f"{where}: {name} is on {t.device}, other tensors on {device}")
         if dtype is not None and t.dtype is not dtype:
             raise BifocalError(1, f"{where}: {name} has type {t.dtype}, expected {dtype}")
         if shape is not None and t.shape != shape and (
                 t.dim() != len(shape) or any(w != -1 and n != w for n, w in zip(t.shape, shape))):
             raise BifocalError(1, f"{where}: {name} has shape {tuple(t.shape)}, expected {shape}")
     return device
+
+
+def _current_stream(device) -> int:
+    """The handle of the device's current stream, without making a Stream object of it where torch can."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device.index) if raw is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 class _On:
@@ -418,14 +428,15 @@ class _On:
 
     def __enter__(self):
         import torch
-        if self.stream is not None or self.device.index != torch.cuda.current_device():
-            guards = [torch.cuda.device(self.device)]
-            if self.stream is not None:
-                guards.append(torch.cuda.stream(self.stream))
-            for g in guards:
-                g.__enter__()
-            self.guards = guards
-        return torch.cuda.current_stream(self.device).cuda_stream if self.stream is None else self.stream.cuda_stream
+        if self.stream is None:
+            if self.device.index != torch.cuda.current_device():
+                self.guards = (torch.cuda.device(self.device),)
+                self.guards[0].__enter__()
+            return _current_stream(self.device)
+        self.guards = (torch.cuda.device(self.device), torch.cuda.stream(self.stream))
+        for g in self.guards:
+            g.__enter__()
+        return self.stream.cuda_stream
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
