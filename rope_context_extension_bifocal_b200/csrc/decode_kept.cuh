@@ -47,7 +47,6 @@ struct KeptArgs {
   int* kpos;                   // [hkv, rows]
   float* kweight;              // [hkv, rows] or null
   CacheRows rows;
-  int page_shift;              // log2 of the page size, -1 when it is not a power of two
   const int* seq_lens;         // [B] slots with the new token's
   const int* positions;        // [B] position of the new token
   int hq, hkv, w0, w_pretrained, mode, window, max_len;
@@ -127,7 +126,7 @@ __global__ void __launch_bounds__(kept::WARPS * 32, GP <= 4 ? 4 : 2) decode_kept
     row = -1;
     pos = seq.now;
     if (slot < s_end) {
-      const int page = a.page_shift >= 0 ? slot >> a.page_shift : slot / a.rows.page_size;
+      const int page = a.rows.page_shift >= 0 ? slot >> a.rows.page_shift : slot / a.rows.page_size;
       const int pg = trow[page];
       if (pg < 0 || pg >= a.rows.pool_pages) {
         report_status(kDevIndex, 71);

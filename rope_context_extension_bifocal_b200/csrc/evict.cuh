@@ -48,7 +48,6 @@ struct EvictArgs {
   int* to;                 // [B, hkv, pitch] cache rows they move to
   int pitch;
   int keys_in_smem;        // keys a CTA has room for
-  int page_shift;          // log2 of the page size, -1 when it is not a power of two
 };
 
 __global__ void __launch_bounds__(ev::THREADS, 1) evict_select_kernel(const __grid_constant__ EvictArgs a) {
@@ -90,7 +89,7 @@ __global__ void __launch_bounds__(ev::THREADS, 1) evict_select_kernel(const __gr
   const int wbeg = min(end, beg + warp * per_warp), wend = min(end, wbeg + per_warp);
   const long long newest = a.positions[b];
   auto row_of = [&](const CacheRows& c, int slot) -> int {
-    const int page = a.page_shift >= 0 ? slot >> a.page_shift : slot / c.page_size;
+    const int page = c.page_shift >= 0 ? slot >> c.page_shift : slot / c.page_size;
     const int pg = c.block_table[static_cast<long long>(b) * c.max_pages + page];
     return pg < 0 || pg >= c.pool_pages ? -1 : pg * c.page_size + (slot - page * c.page_size);
   };

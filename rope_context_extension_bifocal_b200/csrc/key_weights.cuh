@@ -48,6 +48,15 @@ template <int QT>
 constexpr int slots() { return QT == 64 ? 2 : 4; }  // query tiles in the ring
 }  // namespace kw
 
+// A sequence's angle tables. Of pairs 8 c + 2 e and 8 c + 2 e + 1, at [form][e][c] (so that the threads of a row
+// read consecutive 16-byte words): turn fractions {hi, lo, hi, lo} of a position, and {cos, cos, sin, sin} of the
+// angle between rows ROW_STEP apart, in the original and the long-range form.
+template <int P>
+struct AngleTables {
+  static constexpr int ROW_STEP = 256 / (P / 8);
+  float4 step[2][4][P / 8], turn[2][4][P / 8];
+};
+
 struct WeightArgs {
   CUtensorMap qo_hi, qo_lo, ql_hi, ql_lo;  // [hkv][form_rows * g][D] fp16 query forms, box (64, QT, 1), 128-byte swizzle
   const void* q;
@@ -61,6 +70,7 @@ struct WeightArgs {
   __half* forms[4];   // the forms above, as weights_query_kernel writes them: Qo high, low, Ql high, low
   float* nl;          // [hkv][nl_pitch] -lse * log2(e) of the rows of the forms
   int form_rows;      // queries of the forms (g rows each)
+  void* angles;       // [batch] AngleTables of the sequences
   long long nl_pitch;
   float scale_log2;
   float* kweight;     // [hkv, rows]
@@ -68,7 +78,7 @@ struct WeightArgs {
   double omega[64];
 };
 
-// A value as an fp16 and the fp16 rest; `top` as in to_f16.
+// Values as fp16 and the fp16 rest; `top` as in to_f16.
 __device__ __forceinline__ void split_f16(const float (&x)[8], uint4& hi, uint4& lo, __half2& top) {
   hi = to_f16(x, top);
   const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w};
@@ -79,6 +89,22 @@ __device__ __forceinline__ void split_f16(const float (&x)[8], uint4& hi, uint4&
     l[e] = pack_f16x2(x[2 * e] - f.x, x[2 * e + 1] - f.y);
   }
   lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// The same of two values in one register pair.
+__device__ __forceinline__ void split_pair(uint64_t v, uint32_t& hi, uint32_t& lo, __half2& top) {
+  hi = f2_to_f16x2(v);
+  const __half2 h = *reinterpret_cast<const __half2*>(&hi);
+  top = __hmax2_nan(top, __habs2(h));
+  const float2 f = __half22float2(h);
+  lo = f2_to_f16x2(f2_sub(v, f2_pack(f.x, f.y)));
+}
+
+// Elements 2 e, 2 e + 1 of eight inputs as a register pair.
+__device__ __forceinline__ uint64_t pair_of(const Vec8<__nv_bfloat16>& v, int e) { return bf16x2_to_f2((&v.u.x)[e]); }
+__device__ __forceinline__ uint64_t pair_of(const Vec8<float>& v, int e) {
+  const float4& f = e < 2 ? v.a : v.b;
+  return e & 1 ? f2_pack(f.z, f.w) : f2_pack(f.x, f.y);
 }
 
 // First query of sequence b in the forms, a multiple of four so that a tile's log-sum-exps start on a 16-byte
@@ -108,6 +134,24 @@ __global__ void __launch_bounds__(kPlanThreads) weights_query_kernel(const __gri
     return;
   }
   if (!ok) return;
+  // the CTAs share the sequences' angle tables, two of them at a time (a thread a pair and form)
+  for (int b = (blockIdx.x - 1) * (kPlanThreads / (2 * P)) + threadIdx.x / (2 * P); b < a.plan.batch;
+       b += (gridDim.x - 1) * (kPlanThreads / (2 * P))) {
+    const int G = factor_of(a.plan.cu[b + 1] - a.plan.cu[b], a.w_pretrained);
+    const int f = threadIdx.x / P % 2, k = threadIdx.x % P;
+    const TurnStep t = turn_step(f == 1 && a.mode == 0 ? a.omega[k] / G : a.omega[k]);
+    constexpr int on = AngleTables<P>::ROW_STEP;
+    const int m = f == 1 && a.mode != 0 ? on / G : on;  // position aliasing: used where G divides it
+    float c, s;
+    turn_cos_sin(m, static_cast<float>(m), t, c, s);
+    AngleTables<P>& to = static_cast<AngleTables<P>*>(a.angles)[b];
+    float* step = reinterpret_cast<float*>(&to.step[f][k % 8 / 2][k / 8]) + k % 2 * 2;
+    step[0] = __uint_as_float(t.hi);
+    step[1] = t.lo;
+    float* turn = reinterpret_cast<float*>(&to.turn[f][k % 8 / 2][k / 8]) + k % 2;
+    turn[0] = c;
+    turn[2] = s;
+  }
   const int g = a.hq / a.hkv;
   if (threadIdx.x < kw::QROWS) {
     Row x;
@@ -229,7 +273,7 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ __align__(16) float s_nl[NBUF][QT];
   __shared__ float s_sum[128];
-  __shared__ TurnStep s_step[2][P];  // original and long-range form
+  __shared__ AngleTables<P> s_angles;
   __shared__ uint64_t q_full[NSLOT], q_empty[NSLOT], s_full[NBUF], s_free[NBUF], nl_full[NBUF], k_ready, k_free, drain;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int s_abort;
@@ -264,6 +308,24 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
   const int t_lb = lng_pairs ? clamp_t(x_far > 0 ? x_far / QT : 0) : n_t;
   const int n_o = t_oe - t_first, n_l = n_t - t_lb, nv = n_o + n_l;
 
+  // The keys' loads go out first: with 16-bit inputs a thread's rows fit its registers until they are used.
+  constexpr int CPR = P / 8;             // threads a row of the key tile, 8 pairs each
+  constexpr int ROW_STEP = AngleTables<P>::ROW_STEP;  // rows between a thread's
+  constexpr int RPT = 128 / ROW_STEP;    // rows a thread
+  constexpr int RB = sizeof(Tin) == 2 ? RPT : RPT / 2;  // of them loaded together
+  const int c8 = threadIdx.x % CPR, k0 = c8 * 8, row0 = threadIdx.x / CPR;
+  Vec8<Tin> x1[RB], x2[RB];
+  auto load_keys = [&](int i0) {
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      const int row = row0 + (i0 + i) * ROW_STEP;
+      const Tin* src = static_cast<const Tin*>(a.k) + (static_cast<long long>(tile.first + min(j0 + row, L - 1)) * a.hkv + kvh) * D;
+      x1[i].load(src + k0);
+      x2[i].load(src + P + k0);
+    }
+  };
+  if (warp < 8 && nv > 0) load_keys(0);
+
   const uint32_t base = smem_u32(smem);
   const uint32_t k_hi = base, k_lo = base + KTILE, ring = base + 2 * KTILE;
   if (threadIdx.x == 0) {
@@ -282,11 +344,9 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
     mbar_init(&drain, 1);
     fence_barrier_init();
   }
-  if (threadIdx.x < P) {
-    const double om = a.omega[threadIdx.x];
-    s_step[0][threadIdx.x] = turn_step(om);
-    s_step[1][threadIdx.x] = turn_step(a.mode == 0 ? om / G : om);
-  }
+  if (threadIdx.x < sizeof(AngleTables<P>) / 16)
+    reinterpret_cast<float4*>(&s_angles)[threadIdx.x] =
+        reinterpret_cast<const float4*>(static_cast<const AngleTables<P>*>(a.angles) + tile.seq)[threadIdx.x];
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_sh)),
                  "r"(NCOL));
@@ -306,7 +366,7 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
         const int t = tile_of(v), buf = v % NBUF;
         const bool lng = v >= n_o;
         // the buffer's log-sum-exp row is free once its last visit has been summed
-        if (v >= NBUF && !mbar_wait_abortable(&s_free[buf], (v / NBUF - 1) & 1, 100, &s_abort)) break;
+        if (v >= NBUF && !mbar_wait_suspend(&s_free[buf], (v / NBUF - 1) & 1, 100, &s_abort)) break;
         mbar_arrive_expect_tx(&nl_full[buf], QT * 4);
         asm volatile(
             "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
@@ -318,7 +378,7 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
         bool ok = true;
         for (int x = 0; x < fpv; ++x) {
           const int n = fpv * v + x, slot = n % NSLOT;
-          if (n >= NSLOT && !mbar_wait_abortable(&q_empty[slot], (n / NSLOT - 1) & 1, 101, &s_abort)) {
+          if (n >= NSLOT && !mbar_wait_suspend(&q_empty[slot], (n / NSLOT - 1) & 1, 101, &s_abort)) {
             ok = false;
             break;
           }
@@ -350,10 +410,10 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
       };
       for (int v = 0; v < nv; ++v) {
         const int buf = v % NBUF, n0 = fpv * v, hi = n0 % NSLOT, lo = (n0 + 1) % NSLOT;
-        if (v == 0 && !mbar_wait_abortable(&k_ready, 0, 110, &s_abort)) break;
-        if (v == n_o && n_o > 0 && !mbar_wait_abortable(&k_ready, 1, 111, &s_abort)) break;
-        if (v >= NBUF && !mbar_wait_abortable(&s_free[buf], (v / NBUF - 1) & 1, 112, &s_abort)) break;
-        if (!mbar_wait_abortable(&q_full[hi], (n0 / NSLOT) & 1, 113, &s_abort)) break;
+        if (v == 0 && !mbar_wait_suspend(&k_ready, 0, 110, &s_abort)) break;
+        if (v == n_o && n_o > 0 && !mbar_wait_suspend(&k_ready, 1, 111, &s_abort)) break;
+        if (v >= NBUF && !mbar_wait_suspend(&s_free[buf], (v / NBUF - 1) & 1, 112, &s_abort)) break;
+        if (!mbar_wait_suspend(&q_full[hi], (n0 / NSLOT) & 1, 113, &s_abort)) break;
         fence_after();
         const uint32_t d = tmem + buf * QT;
         const uint64_t bh = dq0 + static_cast<uint64_t>(hi * (QTILE >> 4)), bl = dq0 + static_cast<uint64_t>(lo * (QTILE >> 4));
@@ -361,7 +421,7 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
         if (split) {
           product(d, dkl, bh, true);
           mma_commit(&q_empty[hi]);
-          if (!mbar_wait_abortable(&q_full[lo], ((n0 + 1) / NSLOT) & 1, 114, &s_abort)) break;
+          if (!mbar_wait_suspend(&q_full[lo], ((n0 + 1) / NSLOT) & 1, 114, &s_abort)) break;
           fence_after();
           product(d, dkh, bl, true);
           mma_commit(&q_empty[lo]);
@@ -378,51 +438,62 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
     // ------------------------------------------------------------ key tile, then sums
     const int group = warp >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;
-    // The key tile under one branch, split in two: a thread has 8 pairs of every (256 / CPR)-th row; rows past the
-    // sequence are zero. The loads of RB rows are in flight together.
-    auto form_keys = [&](bool lng) {
+    // The key tile under one branch, split in two: a thread has 8 pairs of every ROW_STEP-th row; rows past the
+    // sequence are zero. A row's angles follow from those of the row ROW_STEP before by one rotation (a product of
+    // complex numbers on packed pairs) where the angle is linear in that step: always but for position aliasing
+    // with a G that does not divide it.
+    auto form_keys = [&](bool lng, bool loaded) {
       __half2 top = __float2half2_rn(0.f);
-      constexpr int CPR = P / 8;               // threads a row
-      constexpr int RPT = 128 * CPR / 256;     // rows a thread
-      constexpr int RB = sizeof(Tin) == 2 ? RPT : RPT / 2;
-      const int c8 = threadIdx.x % CPR, k0 = c8 * 8, d2 = P + k0, row0 = threadIdx.x / CPR;
-      TurnStep step[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) step[e] = s_step[lng ? 1 : 0][k0 + e];
+      const int d2 = P + k0, f = lng ? 1 : 0;
+      const bool alias = lng && a.mode != 0;
+      const bool linear = !alias || ROW_STEP % G == 0;
+      uint64_t c2[4], s2[4];
 #pragma unroll 1
       for (int i0 = 0; i0 < RPT; i0 += RB) {
-        Vec8<Tin> x1[RB], x2[RB];
+        if (i0 > 0 || !loaded) load_keys(i0);
 #pragma unroll
         for (int i = 0; i < RB; ++i) {
-          const int row = row0 + (i0 + i) * (256 / CPR);
-          const Tin* src = static_cast<const Tin*>(a.k) +
-                           (static_cast<long long>(tile.first + min(j0 + row, L - 1)) * a.hkv + kvh) * D;
-          x1[i].load(src + k0);
-          x2[i].load(src + P + k0);
-        }
+          const int row = row0 + (i0 + i) * ROW_STEP, j = j0 + row;
+          if (i0 + i == 0 || !linear) {
+            const int m = alias ? j / G : j;
 #pragma unroll
-        for (int i = 0; i < RB; ++i) {
-          const int row = row0 + (i0 + i) * (256 / CPR), j = j0 + row;
-          const int m = lng && a.mode != 0 ? j / G : j;
-          const float mf = static_cast<float>(m), in = j < L ? 1.f : 0.f;
-          float y1[8], y2[8];
+            for (int e = 0; e < 4; ++e) {
+              const float4 t = s_angles.step[f][e][c8];
+              float c[2], s[2];
+              turn_cos_sin(m, static_cast<float>(m), TurnStep{__float_as_uint(t.x), t.y}, c[0], s[0]);
+              turn_cos_sin(m, static_cast<float>(m), TurnStep{__float_as_uint(t.z), t.w}, c[1], s[1]);
+              c2[e] = f2_pack(c[0], c[1]);
+              s2[e] = f2_pack(s[0], s[1]);
+            }
+          } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float c, s;
-            turn_cos_sin(m, mf, step[e], c, s);
-            const float u = x1[i].get(e), v = x2[i].get(e);
-            y1[e] = in != 0.f ? u * c - v * s : 0.f;
-            y2[e] = in != 0.f ? v * c + u * s : 0.f;
+            for (int e = 0; e < 4; ++e) {
+              const float4 t = s_angles.turn[f][e][c8];
+              const uint64_t tc = f2_pack(t.x, t.y), ts = f2_pack(t.z, t.w);
+              const uint64_t nc = f2_sub(f2_mul(c2[e], tc), f2_mul(s2[e], ts));
+              s2[e] = f2_fma(s2[e], tc, f2_mul(c2[e], ts));
+              c2[e] = nc;
+            }
+          }
+          uint32_t h1[4], l1[4], h2[4], l2[4];
+          if (j >= L) {  // its angles stay as they are for the next row
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h1[e] = l1[e] = h2[e] = l2[e] = 0u;
+          } else
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint64_t u = pair_of(x1[i], e), v = pair_of(x2[i], e);
+            split_pair(f2_sub(f2_mul(u, c2[e]), f2_mul(v, s2[e])), h1[e], l1[e], top);
+            split_pair(f2_fma(v, c2[e], f2_mul(u, s2[e])), h2[e], l2[e], top);
           }
           // element d of a row: half d / 64, 16-byte chunk (d % 64) / 8 of its 128 bytes, swizzled
           const uint32_t o1 = (k0 / 64) * HALF + sw128(row, (k0 % 64) / 8), o2 = (d2 / 64) * HALF + sw128(row, (d2 % 64) / 8);
-          uint4 hi, lo;
-          split_f16(y1, hi, lo, top);
-          *reinterpret_cast<uint4*>(smem + o1) = hi;
-          if (split) *reinterpret_cast<uint4*>(smem + KTILE + o1) = lo;
-          split_f16(y2, hi, lo, top);
-          *reinterpret_cast<uint4*>(smem + o2) = hi;
-          if (split) *reinterpret_cast<uint4*>(smem + KTILE + o2) = lo;
+          *reinterpret_cast<uint4*>(smem + o1) = make_uint4(h1[0], h1[1], h1[2], h1[3]);
+          *reinterpret_cast<uint4*>(smem + o2) = make_uint4(h2[0], h2[1], h2[2], h2[3]);
+          if (split) {
+            *reinterpret_cast<uint4*>(smem + KTILE + o1) = make_uint4(l1[0], l1[1], l1[2], l1[3]);
+            *reinterpret_cast<uint4*>(smem + KTILE + o2) = make_uint4(l2[0], l2[1], l2[2], l2[3]);
+          }
         }
       }
       if (!all_finite(top)) report_status(kDevRange, 91);
@@ -430,13 +501,20 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
       __syncwarp();
       if (lane == 0) mbar_arrive(&k_ready);
     };
+    // where this thread's key goes, looked up while the products run
+    long long at = -1;
+    const bool mine = group == 0 && j0 + r < L;
     bool ok = true;
-    if (nv > 0) form_keys(n_o == 0);
+    if (nv > 0) form_keys(n_o == 0, true);
+    if (mine) {
+      at = cache_row(a.rows, tile.seq, j0 + r, tile.first + j0 + r);
+      if (at < 0) report_status(kDevIndex, 92);
+    }
     bool switched = n_o == 0 || n_l == 0;  // one branch only
     auto to_long = [&]() {
       // every product with the local form has been computed before it is overwritten
-      ok = ok && __all_sync(0xffffffffu, mbar_wait_abortable(&k_free, 0, 120, &s_abort));
-      if (ok) form_keys(true);
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_suspend(&k_free, 0, 120, &s_abort));
+      if (ok) form_keys(true, false);
       switched = true;
     };
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
@@ -447,8 +525,8 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
       if (!ok) break;
       const int t = tile_of(v), buf = v % NBUF;
       const bool lng = v >= n_o;
-      if (!__all_sync(0xffffffffu, mbar_wait_abortable(&nl_full[buf], (v / NBUF) & 1, 121, &s_abort) &&
-                                       mbar_wait_abortable(&s_full[buf], (v / NBUF) & 1, 122, &s_abort))) {
+      if (!__all_sync(0xffffffffu, mbar_wait_suspend(&nl_full[buf], (v / NBUF) & 1, 121, &s_abort) &&
+                                       mbar_wait_suspend(&s_full[buf], (v / NBUF) & 1, 122, &s_abort))) {
         ok = false;
         break;
       }
@@ -518,13 +596,8 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
     // the two groups' sums, in a fixed order
     if (group == 1) s_sum[r] = sum;
     asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (group == 0 && j0 + r < L && !*reinterpret_cast<volatile int*>(&s_abort)) {
-      const long long at = cache_row(a.rows, tile.seq, j0 + r, tile.first + j0 + r);
-      if (at < 0)
-        report_status(kDevIndex, 92);
-      else
-        a.kweight[static_cast<long long>(kvh) * a.rows.rows + at] = sum + s_sum[r];
-    }
+    if (mine && at >= 0 && !*reinterpret_cast<volatile int*>(&s_abort))
+      a.kweight[static_cast<long long>(kvh) * a.rows.rows + at] = sum + s_sum[r];
   }
   fence_before();
   __syncthreads();

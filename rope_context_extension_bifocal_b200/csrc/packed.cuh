@@ -17,15 +17,17 @@ namespace bf {
 struct CacheRows {
   const int* block_table;
   int max_pages, page_size, pool_pages;
-  int rows;  // rows of the cache, and the pitch of the per-head arrays [hkv, rows]
+  int rows;        // rows of the cache, and the pitch of the per-head arrays [hkv, rows]
+  int page_shift;  // log2 of the page size, -1 when it is not a power of two (then it is divided by)
 };
 
 // Row of position p of sequence b, or -1 when the table's entry is not a page of the pool.
 __device__ __forceinline__ long long cache_row(const CacheRows& c, int b, int p, int packed_row) {
   if (!c.block_table) return packed_row;
-  const int pg = c.block_table[static_cast<long long>(b) * c.max_pages + p / c.page_size];
+  const int page = c.page_shift >= 0 ? p >> c.page_shift : p / c.page_size;
+  const int pg = c.block_table[static_cast<long long>(b) * c.max_pages + page];
   if (pg < 0 || pg >= c.pool_pages) return -1;
-  return static_cast<long long>(pg) * c.page_size + p % c.page_size;
+  return static_cast<long long>(pg) * c.page_size + (p - page * c.page_size);
 }
 
 struct PlanHeader {

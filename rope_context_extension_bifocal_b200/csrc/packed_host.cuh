@@ -17,14 +17,10 @@ bf_status_t make_cache_rows(int64_t cache_rows, int32_t page_size, const int32_t
   r->max_pages = max_pages;
   r->page_size = page_size;
   r->pool_pages = static_cast<int>(cache_rows / page_size);
-  return BF_OK;
-}
-
-// log2 of a page size, -1 when it is not a power of two (the kernels then divide).
-int page_shift(int page_size) {
+  r->page_shift = -1;
   for (int i = 0; i < 31; ++i)
-    if (page_size == 1 << i) return i;
-  return -1;
+    if (page_size == 1 << i) r->page_shift = i;
+  return BF_OK;
 }
 
 int64_t packed_max_tiles(int64_t total_rows, int64_t batch) {
@@ -341,7 +337,6 @@ bf_status_t decode_kept_impl(const void* q, const void* k_new, const void* v_new
   if (!workspace || !aligned(workspace, 256) || ws_bytes < lay.total) return BF_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const Rope rope = make_rope(p->rope_theta, p->head_dim, 1);
-  a.page_shift = page_shift(page_size);
   // a stage's slots share a page, and are one box of the pool, where pages hold whole stages
   a.boxes = page_size % (bf::kept::STAGE_BYTES / (4 * p->head_dim)) == 0 ? 1 : 0;
   if (a.boxes && (!make_slot_map(&a.k_map, kcache, cache_rows, p->hkv, p->head_dim) ||
@@ -447,7 +442,6 @@ bf_status_t cache_evict_impl(void* kcache, void* vcache, int32_t* kpos, float* k
   a.from = reinterpret_cast<int*>(ws + lay.from);
   a.to = reinterpret_cast<int*>(ws + lay.to);
   a.pitch = lay.pitch;
-  a.page_shift = page_shift(page_size);
   // a CTA for every CTA_SLOTS slots, in clusters of up to 8
   int size = 1;
   while (size < 8 && static_cast<int64_t>(size) * bf::ev::CTA_SLOTS < max_len) size *= 2;
@@ -487,7 +481,7 @@ bf_status_t cache_evict_impl(void* kcache, void* vcache, int32_t* kpos, float* k
 
 // ------------------------------------------------------------------ attention weight of keys
 struct WeightLayout {
-  size_t tiles, forms, form_bytes, nl, total;
+  size_t tiles, angles, forms, form_bytes, nl, total;
   int64_t max_tiles, rows;  // rows: queries of the forms
   int window_pitch;         // of them a sequence, 0: as many as it has rows
 };
@@ -500,7 +494,8 @@ WeightLayout weight_layout(int batch, int T, int obs, const bf_params_t* p) {
   w.window_pitch = pitch * batch <= packed ? static_cast<int>(pitch) : 0;
   w.rows = w.window_pitch ? pitch * batch : packed;
   w.tiles = 256;
-  w.forms = w.tiles + align256(static_cast<size_t>(w.max_tiles) * sizeof(bf::PackedTile));
+  w.angles = w.tiles + align256(static_cast<size_t>(w.max_tiles) * sizeof(bf::PackedTile));
+  w.forms = w.angles + align256(static_cast<size_t>(batch) * (p->head_dim == 128 ? sizeof(bf::AngleTables<64>) : sizeof(bf::AngleTables<32>)));
   w.form_bytes = align256(static_cast<size_t>(w.rows) * p->hq * p->head_dim * 2);
   w.nl = w.forms + 4 * w.form_bytes;
   w.total = w.nl + align256((static_cast<size_t>(w.rows) * (p->hq / p->hkv) + 128) * p->hkv * 4);
@@ -572,6 +567,7 @@ bf_status_t key_weights_impl(const void* q, const void* k, int32_t dtype, const 
   a.w_pretrained = p->w_pretrained;
   a.mode = p->mode;
   a.window = (p->flags & BF_FLAG_WINDOW) ? 1 : 0;
+  a.angles = ws + lay.angles;
   a.nl = reinterpret_cast<float*>(ws + lay.nl);
   a.form_rows = static_cast<int>(lay.rows);
   a.nl_pitch = lay.rows * g + 128;
