@@ -19,14 +19,14 @@
 // the tile has (the local queries first, then the long-range ones); no rotated copy of k is written. The
 // query rows are turned once by weights_query_kernel and arrive by TMA.
 //
-// Warp roles: warps 0..7 form the key tile and then sum (two groups of four warps, one visit each in
-// turn; warp w reads TMEM lanes 32 (w % 4) ..), warp 8 = TMA producer, warp 9 = MMA issuer. A visit is one
-// query tile under one branch. Tensor memory holds four S tiles, shared memory the key tile (high and low
-// part) and a ring of query tiles.
+// Warp roles: the first 8 or 16 warps form the key tile and then sum (groups of four warps, one visit each in
+// turn; warp w reads TMEM lanes 32 (w % 4) ..), then a TMA producer and an MMA issuer. A visit is one
+// query tile under one branch. Shared memory holds the key tile (high and low part) and a ring of query tiles.
 //
 // Few rows (QT = 64): each key tile has a handful of visits and its time is the latency of forming it, so two
-// CTAs share an SM (96 KB and 256 tensor-memory columns each). Many rows (QT = 128): one CTA, four 32 KB query
-// slots; bound by the 16 ex2 a clock (1024 clocks a visit, the product 512).
+// CTAs share an SM (96 KB and 256 tensor-memory columns each). Many rows (QT = 256): one CTA, two 64 KB query slots,
+// two S tiles of 256 columns, each summed by two groups; wide products, because what the issuing thread does between
+// two visits is idle time of the tensor core (with 128 columns it was half of it).
 #pragma once
 #include <type_traits>
 
@@ -40,12 +40,19 @@ namespace bf {
 
 namespace kw {
 constexpr int QROWS = 4;  // query rows a CTA of weights_query_kernel
-constexpr int NBUF = 4;   // S tiles in tensor memory, and log-sum-exp rows in shared memory
-constexpr int NTHREADS = 320;
 constexpr uint32_t HALF = 16384;    // 128 rows of 64 fp16 values
 constexpr int SINGLE_FROM = 16384;  // (query, head) rows from which a single fp16 product is enough
+constexpr int NSLOT = 2;            // query tiles in the ring
+constexpr int NROW = 4;             // rows of log-sum-exps in shared memory
+// S tiles in tensor memory; summing groups of four warps; groups that share a visit, each a range of its columns
 template <int QT>
-constexpr int slots() { return QT == 64 ? 2 : 4; }  // query tiles in the ring
+constexpr int buffers() { return QT == 64 ? 4 : 2; }
+template <int QT>
+constexpr int groups() { return QT == 64 ? 2 : 4; }
+template <int QT>
+constexpr int sharing() { return QT == 64 ? 1 : 4; }
+template <int QT>
+constexpr int threads() { return groups<QT>() * 128 + 64; }
 }  // namespace kw
 
 // A sequence's angle tables. Of pairs 8 c + 2 e and 8 c + 2 e + 1, at [form][e][c] (so that the threads of a row
@@ -53,7 +60,6 @@ constexpr int slots() { return QT == 64 ? 2 : 4; }  // query tiles in the ring
 // angle between rows ROW_STEP apart, in the original and the long-range form.
 template <int P>
 struct AngleTables {
-  static constexpr int ROW_STEP = 256 / (P / 8);
   float4 step[2][4][P / 8], turn[2][4][P / 8];
 };
 
@@ -71,6 +77,7 @@ struct WeightArgs {
   float* nl;          // [hkv][nl_pitch] -lse * log2(e) of the rows of the forms
   int form_rows;      // queries of the forms (g rows each)
   void* angles;       // [batch] AngleTables of the sequences
+  int row_step;       // rows between those of a thread that forms keys
   long long nl_pitch;
   float scale_log2;
   float* kweight;     // [hkv, rows]
@@ -140,8 +147,7 @@ __global__ void __launch_bounds__(kPlanThreads) weights_query_kernel(const __gri
     const int G = factor_of(a.plan.cu[b + 1] - a.plan.cu[b], a.w_pretrained);
     const int f = threadIdx.x / P % 2, k = threadIdx.x % P;
     const TurnStep t = turn_step(f == 1 && a.mode == 0 ? a.omega[k] / G : a.omega[k]);
-    constexpr int on = AngleTables<P>::ROW_STEP;
-    const int m = f == 1 && a.mode != 0 ? on / G : on;  // position aliasing: used where G divides it
+    const int m = f == 1 && a.mode != 0 ? a.row_step / G : a.row_step;  // position aliasing: used where G divides it
     float c, s;
     turn_cos_sin(m, static_cast<float>(m), t, c, s);
     AngleTables<P>& to = static_cast<AngleTables<P>*>(a.angles)[b];
@@ -257,13 +263,15 @@ __device__ __forceinline__ uint64_t exp2_fma2(uint64_t x2) {
 }
 
 template <typename Tin, int D, int QT>
-__global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_kernel(const __grid_constant__ WeightArgs a) {
+__global__ void __launch_bounds__(kw::threads<QT>(), QT == 64 ? 2 : 1) key_weights_kernel(const __grid_constant__ WeightArgs a) {
   using namespace kw;
   using tc::fence_after;
   using tc::fence_before;
   using tc::mma_commit;
   constexpr int P = D / 2;
-  constexpr int NSLOT = slots<QT>();
+  constexpr int NBUF = buffers<QT>(), NG = groups<QT>(), SHARE = sharing<QT>();
+  constexpr int SUMMERS = NG * 4;                // summing warps; then the TMA and the MMA warp
+  constexpr int COLS = QT / SHARE;               // columns of a visit that a group sums
   constexpr uint32_t KTILE = D / 64 * HALF;      // the key operand: 128 rows
   constexpr uint32_t QHALF = QT * 128;           // 64 dimensions of QT query rows
   constexpr uint32_t QTILE = D / 64 * QHALF;
@@ -271,10 +279,10 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
   constexpr uint32_t NCOL = NBUF * QT;           // tensor-memory columns
   constexpr uint32_t IDESC = (1u << 4) | (static_cast<uint32_t>(QT / 8) << 17) | (8u << 24);  // f16 x f16 -> f32, 128 x QT
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ __align__(16) float s_nl[NBUF][QT];
-  __shared__ float s_sum[128];
+  __shared__ __align__(16) float s_nl[NROW][QT];
+  __shared__ float s_sum[NG - 1][128];
   __shared__ AngleTables<P> s_angles;
-  __shared__ uint64_t q_full[NSLOT], q_empty[NSLOT], s_full[NBUF], s_free[NBUF], nl_full[NBUF], k_ready, k_free, drain;
+  __shared__ uint64_t q_full[NSLOT], q_empty[NSLOT], s_full[NBUF], s_free[NBUF], nl_full[NROW], nl_free[NROW], k_ready, k_free, drain;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int s_abort;
 
@@ -310,9 +318,9 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
 
   // The keys' loads go out first: with 16-bit inputs a thread's rows fit its registers until they are used.
   constexpr int CPR = P / 8;             // threads a row of the key tile, 8 pairs each
-  constexpr int ROW_STEP = AngleTables<P>::ROW_STEP;  // rows between a thread's
+  constexpr int ROW_STEP = SUMMERS * 32 / CPR;        // rows between a thread's
   constexpr int RPT = 128 / ROW_STEP;    // rows a thread
-  constexpr int RB = sizeof(Tin) == 2 ? RPT : RPT / 2;  // of them loaded together
+  constexpr int RB = sizeof(Tin) == 2 || RPT == 1 ? RPT : RPT / 2;  // of them loaded together
   const int c8 = threadIdx.x % CPR, k0 = c8 * 8, row0 = threadIdx.x / CPR;
   Vec8<Tin> x1[RB], x2[RB];
   auto load_keys = [&](int i0) {
@@ -324,7 +332,7 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
       x2[i].load(src + P + k0);
     }
   };
-  if (warp < 8 && nv > 0) load_keys(0);
+  if (warp < SUMMERS && nv > 0) load_keys(0);
 
   const uint32_t base = smem_u32(smem);
   const uint32_t k_hi = base, k_lo = base + KTILE, ring = base + 2 * KTILE;
@@ -336,10 +344,13 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
     }
     for (int i = 0; i < NBUF; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], 4);
-      mbar_init(&nl_full[i], 1);
+      mbar_init(&s_free[i], 4 * SHARE);
     }
-    mbar_init(&k_ready, 8);
+    for (int i = 0; i < NROW; ++i) {
+      mbar_init(&nl_full[i], 1);
+      mbar_init(&nl_free[i], 4 * SHARE);
+    }
+    mbar_init(&k_ready, SUMMERS);
     mbar_init(&k_free, 1);
     mbar_init(&drain, 1);
     fence_barrier_init();
@@ -347,7 +358,7 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
   if (threadIdx.x < sizeof(AngleTables<P>) / 16)
     reinterpret_cast<float4*>(&s_angles)[threadIdx.x] =
         reinterpret_cast<const float4*>(static_cast<const AngleTables<P>*>(a.angles) + tile.seq)[threadIdx.x];
-  if (warp == 9) {
+  if (warp == SUMMERS + 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_sh)),
                  "r"(NCOL));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -358,15 +369,15 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
   const uint32_t tmem = tmem_base_sh;
   auto tile_of = [&](int v) { return v >= n_o ? t_lb + v - n_o : t_first + v; };
 
-  if (warp == 8) {
+  if (warp == SUMMERS) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       uint32_t used = 0, par = 0, nl_used = 0, nl_par = 0;
       for (int v = 0; v < nv; ++v) {
-        const int t = tile_of(v), buf = v % NBUF;
+        const int t = tile_of(v), buf = v % NROW;
         const bool lng = v >= n_o;
-        // the buffer's log-sum-exp row is free once its last visit has been summed
-        if (v >= NBUF && !mbar_wait_suspend(&s_free[buf], (v / NBUF - 1) & 1, 100, &s_abort)) break;
+        // a log-sum-exp row is free once its last visit has been summed
+        if (v >= NROW && !mbar_wait_suspend(&nl_free[buf], (v / NROW - 1) & 1, 100, &s_abort)) break;
         mbar_arrive_expect_tx(&nl_full[buf], QT * 4);
         asm volatile(
             "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
@@ -395,10 +406,10 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
       // every copy issued has landed before the CTA may exit
       for (int i = 0; i < NSLOT; ++i)
         if (used & (1u << i)) mbar_wait_sleepy(&q_full[i], ((par >> i) & 1u) ^ 1u, 102);
-      for (int i = 0; i < NBUF; ++i)
+      for (int i = 0; i < NROW; ++i)
         if (nl_used & (1u << i)) mbar_wait_sleepy(&nl_full[i], ((nl_par >> i) & 1u) ^ 1u, 103);
     }
-  } else if (warp == 9) {
+  } else if (warp == SUMMERS + 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0 && nv > 0) {
       const uint64_t dkh = tc::k_desc(k_hi, 0), dkl = tc::k_desc(k_lo, 0), dq0 = tc::k_desc(ring, 0);
@@ -408,28 +419,32 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
           tc2::mma_ss(d, da + (((kk >> 2) * HALF + (kk & 3) * 32) >> 4), db + (((kk >> 2) * QHALF + (kk & 3) * 32) >> 4),
                       IDESC, acc || kk > 0);
       };
+      // Everything between two visits' products is time the tensor core idles (an MMA is issued only once the one
+      // before it has been taken), so the loop keeps its ring positions and phases instead of dividing.
+      int buf = 0, slot = 0;
+      uint32_t buf_ph = 1, slot_ph = 0;  // phase of a buffer's last release, of a slot's fill
       for (int v = 0; v < nv; ++v) {
-        const int buf = v % NBUF, n0 = fpv * v, hi = n0 % NSLOT, lo = (n0 + 1) % NSLOT;
-        if (v == 0 && !mbar_wait_suspend(&k_ready, 0, 110, &s_abort)) break;
-        if (v == n_o && n_o > 0 && !mbar_wait_suspend(&k_ready, 1, 111, &s_abort)) break;
-        if (v >= NBUF && !mbar_wait_suspend(&s_free[buf], (v / NBUF - 1) & 1, 112, &s_abort)) break;
-        if (!mbar_wait_suspend(&q_full[hi], (n0 / NSLOT) & 1, 113, &s_abort)) break;
+        if (v == 0 && !mbar_wait_abortable(&k_ready, 0, 110, &s_abort)) break;
+        if (v == n_o && n_o > 0 && !mbar_wait_abortable(&k_ready, 1, 111, &s_abort)) break;
+        if (v >= NBUF && !mbar_wait_abortable(&s_free[buf], buf_ph, 112, &s_abort)) break;
+        if (!mbar_wait_abortable(&q_full[slot], slot_ph, 113, &s_abort)) break;
         fence_after();
         const uint32_t d = tmem + buf * QT;
-        const uint64_t bh = dq0 + static_cast<uint64_t>(hi * (QTILE >> 4)), bl = dq0 + static_cast<uint64_t>(lo * (QTILE >> 4));
+        const uint64_t bh = dq0 + static_cast<uint64_t>(slot * (QTILE >> 4));
         product(d, dkh, bh, false);
+        if (split) product(d, dkl, bh, true);
+        mma_commit(&q_empty[slot]);
+        if (++slot == NSLOT) slot = 0, slot_ph ^= 1u;
         if (split) {
-          product(d, dkl, bh, true);
-          mma_commit(&q_empty[hi]);
-          if (!mbar_wait_suspend(&q_full[lo], ((n0 + 1) / NSLOT) & 1, 114, &s_abort)) break;
+          if (!mbar_wait_abortable(&q_full[slot], slot_ph, 114, &s_abort)) break;
           fence_after();
-          product(d, dkh, bl, true);
-          mma_commit(&q_empty[lo]);
-        } else {
-          mma_commit(&q_empty[hi]);
+          product(d, dkh, dq0 + static_cast<uint64_t>(slot * (QTILE >> 4)), true);
+          mma_commit(&q_empty[slot]);
+          if (++slot == NSLOT) slot = 0, slot_ph ^= 1u;
         }
         mma_commit(&s_full[buf]);
         if (v == n_o - 1 && n_l > 0) mma_commit(&k_free);
+        if (++buf == NBUF) buf = 0, buf_ph ^= 1u;
       }
       mma_commit(&drain);
       mbar_wait(&drain, 0, 115);
@@ -437,6 +452,7 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
   } else {
     // ------------------------------------------------------------ key tile, then sums
     const int group = warp >> 2, quad = warp & 3;
+    const int col0 = group % SHARE * COLS;
     const int r = quad * 32 + lane;
     // The key tile under one branch, split in two: a thread has 8 pairs of every ROW_STEP-th row; rows past the
     // sequence are zero. A row's angles follow from those of the row ROW_STEP before by one rotation (a product of
@@ -519,32 +535,39 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
     };
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const float sc = a.scale_log2;
+    // Query i sees key j under the local branch from i = j on, under the long-range one from i = j + w0 on: as rows
+    // (i - start) g, for this thread's key and for the tile's last and first.
+    auto row_of = [&](long long i) { return static_cast<int>(min(max((i - start) * g, 0LL), 0x7fffffffLL)); };
+    const int own_seen = row_of(j0 + r), own_far = row_of(static_cast<long long>(j0) + r + w0);
+    const int all_seen = row_of(j0 + 127), all_far = row_of(static_cast<long long>(j0) + 127 + w0);
+    const int all_near = row_of(static_cast<long long>(j0) + w0);
     float sum = 0.f;
-    for (int v = group; v < nv && ok; v += 2) {
+    for (int v = group / SHARE; v < nv && ok; v += NG / SHARE) {
       if (v >= n_o && !switched) to_long();
       if (!ok) break;
-      const int t = tile_of(v), buf = v % NBUF;
+      const int t = tile_of(v), buf = v % NBUF, nlr = v % NROW;
       const bool lng = v >= n_o;
-      if (!__all_sync(0xffffffffu, mbar_wait_suspend(&nl_full[buf], (v / NBUF) & 1, 121, &s_abort) &&
+      if (!__all_sync(0xffffffffu, mbar_wait_suspend(&nl_full[nlr], (v / NROW) & 1, 121, &s_abort) &&
                                        mbar_wait_suspend(&s_full[buf], (v / NBUF) & 1, 122, &s_abort))) {
         ok = false;
         break;
       }
       fence_after();
-      const int r0 = t * QT, i0 = start + r0 / g, i1 = start + (r0 + QT - 1) / g;  // first and last query
-      const int dmin = i0 - (j0 + 127), dmax = i1 - j0;
-      const int valid = min(QT, rows - r0);
-      const uint32_t s_addr = lane_addr + buf * QT;
-      // Column c holds query i0 + (rem + c) / g; its distance i - j grows with c, so the columns that count are one
-      // range [c_lo, c_hi): (rem + c) / g >= x is c >= x g - rem.
-      int c_lo = 0, c_hi = QT;
-      const bool whole = dmin >= 0 && valid == QT && (lng ? dmin >= w0 : dmax < w0);
+      const int r0 = t * QT + col0;  // this group's columns of the visit: rows r0 ..
+      // the thread's scores into registers at once: the tensor core gets the S tile back before they are summed
+      float s[COLS];
+#pragma unroll
+      for (int c0 = 0; c0 < COLS; c0 += 32) tc::tmem_ld32(lane_addr + buf * QT + col0 + c0, s + c0);
+#pragma unroll
+      for (int c0 = 0; c0 < COLS; c0 += 32) tc::wait_ld32(s + c0);
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_free[buf]);
+      const bool whole = r0 + COLS <= rows && (lng ? r0 >= all_far : r0 >= all_seen && r0 + COLS <= all_near);
+      int c_lo = 0, c_hi = COLS;
       if (!whole) {
-        const int d0 = i0 - j0 - r, rem = r0 % g;
-        const long long lo = (static_cast<long long>(lng ? w0 : 0) - d0) * g - rem;
-        const long long hi = (static_cast<long long>(w0) - d0) * g - rem;
-        c_lo = static_cast<int>(min(max(lo, 0LL), static_cast<long long>(QT)));
-        c_hi = lng ? valid : static_cast<int>(min(max(hi, 0LL), static_cast<long long>(valid)));
+        c_lo = max((lng ? own_far : own_seen) - r0, 0);
+        c_hi = min(COLS, (lng ? rows : min(rows, own_far)) - r0);
       }
       auto add_up = [&](auto masked) {
         const uint64_t sc2 = f2_pack(sc, sc);
@@ -552,62 +575,56 @@ __global__ void __launch_bounds__(kw::NTHREADS, QT == 64 ? 2 : 1) key_weights_ke
         uint64_t acc[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) acc[u] = f2_pack(0.f, 0.f);
-        float s[2][32];
-        tc::tmem_ld32(s_addr, s[0]);
+        const ulonglong2* nl2 = reinterpret_cast<const ulonglong2*>(&s_nl[nlr][col0]);
 #pragma unroll
-        for (int c0 = 0; c0 < QT; c0 += 32) {
-          tc::wait_ld32(s[(c0 / 32) & 1]);
-          if (c0 + 32 < QT) tc::tmem_ld32(s_addr + c0 + 32, s[(c0 / 32 + 1) & 1]);
-          const float* x = s[(c0 / 32) & 1];
-          const ulonglong2* nl2 = reinterpret_cast<const ulonglong2*>(&s_nl[buf][c0]);
-#pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            const ulonglong2 nl = nl2[c / 4];
-            float p[4];
-            f2_unpack(f2_fma(f2_pack(x[c], x[c + 1]), sc2, nl.x), p[0], p[1]);
-            const uint64_t x23 = f2_fma(f2_pack(x[c + 2], x[c + 3]), sc2, nl.y);
-            if (!decltype(masked)::value && c % 8 == 4) {
-              // a quarter of the powers on the FMA pipe: the ex2 unit is what the loop waits for
-              acc[(c / 2) & 3] = f2_add(acc[(c / 2) & 3], f2_pack(fast_exp2(p[0]), fast_exp2(p[1])));
-              acc[(c / 2 + 1) & 3] = f2_add(acc[(c / 2 + 1) & 3], exp2_fma2(x23));
-              continue;
-            }
-            f2_unpack(x23, p[2], p[3]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              p[e] = fast_exp2(p[e]);
-              if (decltype(masked)::value) p[e] = static_cast<uint32_t>(c0 + c + e - c_lo) < span ? p[e] : 0.f;
-            }
-            acc[(c / 2) & 3] = f2_add(acc[(c / 2) & 3], f2_pack(p[0], p[1]));
-            acc[(c / 2 + 1) & 3] = f2_add(acc[(c / 2 + 1) & 3], f2_pack(p[2], p[3]));
+        for (int c = 0; c < COLS; c += 4) {
+          const ulonglong2 nl = nl2[c / 4];
+          float p[4];
+          f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), sc2, nl.x), p[0], p[1]);
+          const uint64_t x23 = f2_fma(f2_pack(s[c + 2], s[c + 3]), sc2, nl.y);
+          if (!decltype(masked)::value && c % 16 == 4) {
+            // an eighth of the powers on the FMA pipe, about where the ex2 unit and the issue slots are equally busy
+            acc[(c / 2) & 3] = f2_add(acc[(c / 2) & 3], f2_pack(fast_exp2(p[0]), fast_exp2(p[1])));
+            acc[(c / 2 + 1) & 3] = f2_add(acc[(c / 2 + 1) & 3], exp2_fma2(x23));
+            continue;
           }
+          f2_unpack(x23, p[2], p[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p[e] = fast_exp2(p[e]);
+            if (decltype(masked)::value) p[e] = static_cast<uint32_t>(c + e - c_lo) < span ? p[e] : 0.f;
+          }
+          acc[(c / 2) & 3] = f2_add(acc[(c / 2) & 3], f2_pack(p[0], p[1]));
+          acc[(c / 2 + 1) & 3] = f2_add(acc[(c / 2 + 1) & 3], f2_pack(p[2], p[3]));
         }
         float lo, hi;
         f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), lo, hi);
         return lo + hi;
       };
       const float part = whole ? add_up(std::false_type()) : add_up(std::true_type());
-      fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s_free[buf]);
+      if (lane == 0) mbar_arrive(&nl_free[nlr]);
       sum += part;
     }
     if (!switched && ok) to_long();
-    // the two groups' sums, in a fixed order
-    if (group == 1) s_sum[r] = sum;
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (mine && at >= 0 && !*reinterpret_cast<volatile int*>(&s_abort))
-      a.kweight[static_cast<long long>(kvh) * a.rows.rows + at] = sum + s_sum[r];
+    // the groups' sums, in a fixed order
+    if (group > 0) s_sum[group - 1][r] = sum;
+    asm volatile("bar.sync 1, %0;" ::"n"(SUMMERS * 32) : "memory");
+    if (mine && at >= 0 && !*reinterpret_cast<volatile int*>(&s_abort)) {
+#pragma unroll
+      for (int i = 0; i < NG - 1; ++i) sum += s_sum[i][r];
+      a.kweight[static_cast<long long>(kvh) * a.rows.rows + at] = sum;
+    }
   }
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(NCOL));
+  if (warp == SUMMERS + 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(NCOL));
 }
 
 template <int D, int QT>
 constexpr int key_weights_smem_bytes() {
-  return (D / 64) * (2 * static_cast<int>(kw::HALF) + kw::slots<QT>() * QT * 128);
+  return (D / 64) * (2 * static_cast<int>(kw::HALF) + kw::NSLOT * QT * 128);
 }
 
 }  // namespace bf

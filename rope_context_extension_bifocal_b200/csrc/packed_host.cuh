@@ -498,7 +498,7 @@ WeightLayout weight_layout(int batch, int T, int obs, const bf_params_t* p) {
   w.forms = w.angles + align256(static_cast<size_t>(batch) * (p->head_dim == 128 ? sizeof(bf::AngleTables<64>) : sizeof(bf::AngleTables<32>)));
   w.form_bytes = align256(static_cast<size_t>(w.rows) * p->hq * p->head_dim * 2);
   w.nl = w.forms + 4 * w.form_bytes;
-  w.total = w.nl + align256((static_cast<size_t>(w.rows) * (p->hq / p->hkv) + 128) * p->hkv * 4);
+  w.total = w.nl + align256((static_cast<size_t>(w.rows) * (p->hq / p->hkv) + 256) * p->hkv * 4);
   return w;
 }
 
@@ -508,7 +508,7 @@ cudaError_t launch_weights_qt(const bf::WeightArgs& a, cudaStream_t st) {
   auto kern = bf::key_weights_kernel<Tin, D, QT>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(a.plan.max_tiles) * a.hkv), dim3(bf::kw::NTHREADS), smem, st, a);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(a.plan.max_tiles) * a.hkv), dim3(bf::kw::threads<QT>()), smem, st, a);
 }
 
 template <typename Tin, int D>
@@ -518,7 +518,7 @@ cudaError_t launch_weights(const bf::WeightArgs& a, int qt, cudaStream_t st) {
                                    dim3(static_cast<unsigned>((units + bf::kw::QROWS - 1) / bf::kw::QROWS + 1)),
                                    dim3(bf::kPlanThreads), 0, st, a);
   if (e != cudaSuccess) return e;
-  return qt == 64 ? launch_weights_qt<Tin, D, 64>(a, st) : launch_weights_qt<Tin, D, 128>(a, st);
+  return qt == 64 ? launch_weights_qt<Tin, D, 64>(a, st) : launch_weights_qt<Tin, D, 256>(a, st);
 }
 
 bf_status_t key_weights_impl(const void* q, const void* k, int32_t dtype, const float* lse, int32_t total_rows,
@@ -546,7 +546,7 @@ bf_status_t key_weights_impl(const void* q, const void* k, int32_t dtype, const 
   if (lay.max_tiles * p->hkv > 0x7fffffffLL || lay.rows * g > 0x7ffffe00LL || p->hq > 65535)
     return BF_ERR_UNSUPPORTED;
   // few rows a key tile: 64-row query tiles, two CTAs an SM
-  const int qt = static_cast<int64_t>(obs) * g <= 512 ? 64 : 128;
+  const int qt = static_cast<int64_t>(obs) * g <= 512 ? 64 : 256;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int D = p->head_dim;
@@ -568,9 +568,10 @@ bf_status_t key_weights_impl(const void* q, const void* k, int32_t dtype, const 
   a.mode = p->mode;
   a.window = (p->flags & BF_FLAG_WINDOW) ? 1 : 0;
   a.angles = ws + lay.angles;
+  a.row_step = (qt == 64 ? bf::kw::groups<64>() : bf::kw::groups<256>()) * 128 / (D / 16);
   a.nl = reinterpret_cast<float*>(ws + lay.nl);
   a.form_rows = static_cast<int>(lay.rows);
-  a.nl_pitch = lay.rows * g + 128;
+  a.nl_pitch = lay.rows * g + 256;
   a.scale_log2 = scale_log2(p);
   // heaviest tiles first over all heads while their query forms (two, fp16) fit in L2 together
   a.head_major = 4 * lay.rows * p->hq * D > (96LL << 20) ? 1 : 0;
