@@ -234,7 +234,7 @@ BF_API bf_status_t bifocal_prefill_chunk_paged(const void* q, const void* k, con
  *   q    [total_rows, hq,  D] raw, dtype;  k, v [total_rows, hkv, D] raw, dtype
  *   cu_seqlens [batch + 1] int32 (device): sequence b is rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1; a
  *          sequence may be empty; rows before cu_seqlens[0] and from cu_seqlens[batch] on belong to none:
- *          they are not read, and nothing is written for them
+ *          nothing of them is used (they may hold anything), and nothing is written for them
  *   max_len: an upper bound of every L_b (host)
  *   out  [total_rows, hq, D] bf16, written;  lse [hq, total_rows] fp32, written (may be NULL)
  *   kcache, vcache [cache_rows, hkv, D] bf16 (both or neither): every key under the ORIGINAL RoPE and its
@@ -326,7 +326,8 @@ BF_API bf_status_t bifocal_decode_paged(const void* q, const void* k_new, const 
  *   workspace / ws_bytes: >= bifocal_key_weights_workspace_size(batch, total_rows, max_len, obs, p), 256-byte aligned
  *          (forms of the queries that count: four fp16 copies).
  * Scores are formed from operands split in two fp16 parts (about 2^-21 relative), not from the single fp16
- * operands of the prefill. Errors on the device as for bifocal_prefill_packed; |q| or |k| from 65520 on is
+ * operands of the prefill; from 16384 (query, head) rows a sequence on, the queries are single fp16 values, whose
+ * roundings average out over so many. Errors on the device as for bifocal_prefill_packed; |q| or |k| from 65520 on is
  * reported as BF_ERR_RANGE. Flags: BF_FLAG_WINDOW drops the long-range pairs (any head_dim and group).
  * Errors: as bifocal_prefill_packed; BF_ERR_INVALID also for NULL lse or kweight and obs < 1. */
 BF_API size_t bifocal_key_weights_workspace_size(int32_t batch, int32_t total_rows, int32_t max_len, int32_t obs,
@@ -354,7 +355,8 @@ BF_API bf_status_t bifocal_key_weights(const void* q, const void* k, int32_t dty
  *   dst_block_table [batch, dst_max_pages] (device): the i-th kept slot is copied to slot i under this
  *          table (pages of the same pool, dst_max_pages * page_size >= min(max_len, budget)); the source rows
  *          stay as they are. Its pages must be none of those the call reads.
- * No page may appear twice among the rows written. Rows that receive no kept slot are left as they were.
+ * No page may appear twice among the rows written: sequences that share pages (a common prefix) are cut to pages
+ * of their own. Rows that receive no kept slot are left as they were.
  *   workspace / ws_bytes: >= bifocal_cache_evict_workspace_size(batch, hkv, max_len, budget), 256-byte aligned.
  * A length outside [0, max_len] is reported as BF_ERR_INDEX by bifocal_last_device_error and that sequence left
  * as it is (new_lens[b] = seq_lens[b]); a table entry outside the pool likewise, its slots rank last and
@@ -383,8 +385,9 @@ BF_API bf_status_t bifocal_cache_evict(void* kcache, void* vcache, int32_t* kpos
  *   block_table [batch, max_pages] int32 (device), page_size >= 1, max_pages * page_size >= max_len
  *   out [batch, hq, D] bf16;  lse [batch, hq] fp32 (may be NULL)
  *   workspace / ws_bytes: >= bifocal_decode_kept_workspace_size(batch, max_len, kweight != NULL, p), 256-byte aligned.
- * Scores, softmax and weights are formed in fp32 (no fp16 operands). Slots past a sequence's length are
- * not read. A length or position out of range is reported as BF_ERR_INDEX by bifocal_last_device_error, appends
+ * Sequences may share pages that neither appends to, but not with kweight (both would add to the same places).
+ * Scores, softmax and weights are formed in fp32 (no fp16 operands). What slots past a sequence's length hold is
+ * not used. A length or position out of range is reported as BF_ERR_INDEX by bifocal_last_device_error, appends
  * nothing and gives NaN as that sequence's output; a table entry outside the pool is reported, its keys
  * and values read as zeros and nothing of its rows is written.
  * Flags: BF_FLAG_WINDOW keeps only keys with p_b - j < w0, under the original RoPE (w0 >= 1); the others

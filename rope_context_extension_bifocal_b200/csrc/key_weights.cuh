@@ -11,9 +11,11 @@
 //
 // Precision. A single fp16 rounding of the rotated operands moves a score by about 3e-4, and so a weight
 // summed from few queries by as much, relative. Each operand is therefore split into an fp16 value and the
-// fp16 rest, and S = Kh Qh + Kl Qh + Kh Ql (the term left out is 2^-22): scores exact to about 1e-6. The errors
-// of a sum of many terms average out as one over the root of their number, so from SINGLE_FROM (query,
-// head) rows on one product is enough: 3e-4 / 128 (a third of the tensor work and half the query bytes).
+// fp16 rest, and S = Kh Qh + Kl Qh + Kh Ql (the term left out is 2^-22): scores exact to about 1e-6. A key's own
+// rounding shifts all its scores alike (the queries that attend to it lean its way), so its low part is always
+// needed: without it weights are 3e-5 off however many queries there are. The queries' roundings are independent
+// and average out: from ROUNDED_FROM (query, head) rows on Kh Ql is left out (a third of the tensor work and half the
+// query bytes), and weights are within 6e-6.
 //
 // Keys come raw from global memory and are turned by the softmax warps themselves, once for each branch
 // the tile has (the local queries first, then the long-range ones); no rotated copy of k is written. The
@@ -41,7 +43,7 @@ namespace bf {
 namespace kw {
 constexpr int QROWS = 4;  // query rows a CTA of weights_query_kernel
 constexpr uint32_t HALF = 16384;    // 128 rows of 64 fp16 values
-constexpr int SINGLE_FROM = 16384;  // (query, head) rows from which a single fp16 product is enough
+constexpr int ROUNDED_FROM = 16384; // (query, head) rows from which the queries' low parts are left out
 constexpr int NSLOT = 2;            // query tiles in the ring
 constexpr int NROW = 4;             // rows of log-sum-exps in shared memory
 // S tiles in tensor memory; summing groups of four warps; groups that share a visit, each a range of its columns
@@ -173,7 +175,7 @@ __global__ void __launch_bounds__(kPlanThreads) weights_query_kernel(const __gri
         x.r = first + x.p;
         x.G = factor_of(n, a.w_pretrained);
         x.lng = !a.window && has_long_pairs(n, x.G, a.w0);
-        x.low = static_cast<long long>(cnt) * g < kw::SINGLE_FROM;
+        x.low = static_cast<long long>(cnt) * g < kw::ROUNDED_FROM;
       }
     }
     s_row[threadIdx.x] = x;
@@ -303,8 +305,8 @@ __global__ void __launch_bounds__(kw::threads<QT>(), QT == 64 ? 2 : 1) key_weigh
   const int w0 = (a.window || lng_pairs) ? a.w0 : kAllLocal;
   const int rows = cnt * g;              // (query, head) rows
   const int qrow = first_query(a, tile.seq, tile.first) * g;  // their first row in the forms
-  const bool split = rows < SINGLE_FROM;
-  const int fpv = split ? 2 : 1;         // ring fills a visit
+  const bool low = rows < ROUNDED_FROM;  // the queries' low parts count
+  const int fpv = low ? 2 : 1;           // ring fills a visit
   // Query tile t holds rows QT t .. QT t + QT - 1: queries start + QT t / g .. start + (QT t + QT - 1) / g. Tiles
   // [t_first, t_oe) have local pairs with these keys, tiles [t_lb, n_t) long-range ones; a tile in both is
   // visited under either branch.
@@ -432,10 +434,10 @@ __global__ void __launch_bounds__(kw::threads<QT>(), QT == 64 ? 2 : 1) key_weigh
         const uint32_t d = tmem + buf * QT;
         const uint64_t bh = dq0 + static_cast<uint64_t>(slot * (QTILE >> 4));
         product(d, dkh, bh, false);
-        if (split) product(d, dkl, bh, true);
+        product(d, dkl, bh, true);
         mma_commit(&q_empty[slot]);
         if (++slot == NSLOT) slot = 0, slot_ph ^= 1u;
-        if (split) {
+        if (low) {
           if (!mbar_wait_abortable(&q_full[slot], slot_ph, 114, &s_abort)) break;
           fence_after();
           product(d, dkh, dq0 + static_cast<uint64_t>(slot * (QTILE >> 4)), true);
@@ -506,10 +508,8 @@ __global__ void __launch_bounds__(kw::threads<QT>(), QT == 64 ? 2 : 1) key_weigh
           const uint32_t o1 = (k0 / 64) * HALF + sw128(row, (k0 % 64) / 8), o2 = (d2 / 64) * HALF + sw128(row, (d2 % 64) / 8);
           *reinterpret_cast<uint4*>(smem + o1) = make_uint4(h1[0], h1[1], h1[2], h1[3]);
           *reinterpret_cast<uint4*>(smem + o2) = make_uint4(h2[0], h2[1], h2[2], h2[3]);
-          if (split) {
-            *reinterpret_cast<uint4*>(smem + KTILE + o1) = make_uint4(l1[0], l1[1], l1[2], l1[3]);
-            *reinterpret_cast<uint4*>(smem + KTILE + o2) = make_uint4(l2[0], l2[1], l2[2], l2[3]);
-          }
+          *reinterpret_cast<uint4*>(smem + KTILE + o1) = make_uint4(l1[0], l1[1], l1[2], l1[3]);
+          *reinterpret_cast<uint4*>(smem + KTILE + o2) = make_uint4(l2[0], l2[1], l2[2], l2[3]);
         }
       }
       if (!all_finite(top)) report_status(kDevRange, 91);

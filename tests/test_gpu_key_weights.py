@@ -126,27 +126,32 @@ def test_neighbours_and_earlier_queries_do_not_leak():
     bfl.last_device_error()
 
 
-def test_many_queries_use_one_product():
-    """From 16384 (query, head) rows on the operands are single fp16 values: a term is off by at most scale
-    (2^-10 + 2^-20) sum |q_d k_d| of itself, at random, so a sum of n comparable terms by that over sqrt(n). The error
-    over all keys is held to a fourteenth of the worst term's (terms average 2^-11 / sqrt(3) twice, a third of the worst
-    of it, and every key has some terms of its own to average over, the median one hundreds)."""
+def test_many_queries():
+    """From 16384 (query, head) rows on the queries are single fp16 values. Rounding element d moves it by at most
+    2^-11 of itself, evenly spread: 2^-11 / sqrt(3) in the root mean square. A score is then off by a standard deviation of
+    s_ij = scale 2^-11 / sqrt(3) (sum_d q_d^2 k_d^2)^(1/2), independently from query to query, and the weights' error has the
+    norm (sum_ij p_ij^2 s_ij^2)^(1/2); one and a half times that, and what split operands leave, is the bound. A single term
+    is off by at most scale 2^-11 sum |q_d k_d| of itself."""
     L, hq, hkv, w0, wp = 2100, 8, 1, 300, 700
     g = si.generator(77)
     q, k = torch.randn(L, hq, 128, generator=g).bfloat16(), torch.randn(L, hkv, 128, generator=g).bfloat16()
-    x, _ = scores(q.double().numpy(), k.double().numpy(), w0, wp, si.FREQ_INTERP, False)
+    x, size = scores(q.double().numpy(), k.double().numpy(), w0, wp, si.FREQ_INTERP, False)
     m = x.max(2)
     l = (m + np.log(np.exp(x - m[..., None]).sum(2))).astype(np.float32)
-    want = np.exp(x - l[..., None].astype(np.float64)).sum((0, 1))
-    # sum |q_d k_d| under any rotation is at most the sum over pairs of |q_pair| |k_pair|
+    p = np.exp(x - l[..., None].astype(np.float64))
+    want = p.sum((0, 1))
+    # under any rotation |q_d k_d| sums, and its squares sum, to at most those of the pairs' lengths
     pair = [np.linalg.norm(np.stack([y[..., :64], y[..., 64:]]), axis=0).reshape(-1, 64) for y in (q.double().numpy(), k.double().numpy())]
-    term = (2.0 ** -10 + 2.0 ** -20) / math.sqrt(128) * (pair[0] @ pair[1].T).max()
+    term = 2.0 ** -11 / math.sqrt(128) * (pair[0] @ pair[1].T).max()
+    spread2 = 2.0 ** -22 / (3 * 128) * (pair[0] ** 2 @ (pair[1] ** 2).T).reshape(L, hq, L).transpose(1, 0, 2)
     cu = torch.tensor([0, L], dtype=torch.int32).cuda()
     got = bfl.bifocal_key_weights(q.cuda(), k.cuda(), torch.from_numpy(l).cuda(), cu, L, L, w0=w0, w_pretrained=wp, theta=THETA)
     assert bfl.last_device_error() == 0
     err = got[0].cpu().double().numpy() - want
-    assert np.all(np.abs(err) <= (term + 4e-6) * want)
-    assert np.linalg.norm(err) <= term / 14 * np.linalg.norm(want)
+    assert np.all(np.abs(err) <= (term + EPS * size + 4e-6) * want)
+    bound = 1.5 * math.sqrt((p ** 2 * spread2).sum()) + (EPS * size / 16 + 1e-6) * np.linalg.norm(want)
+    assert bound <= 2.7e-5 * np.linalg.norm(want)  # tight enough to see the keys' low parts missing (3e-5)
+    assert np.linalg.norm(err) <= bound
 
 
 def test_sum_is_the_number_of_queries():
