@@ -475,15 +475,13 @@ __global__ void __launch_bounds__(kept::WARPS * 32, GP <= 4 ? 4 : 2) decode_kept
 }
 
 // Merges the ranges' partial results and adds the weights. CTA (x, kv head, sequence): every CTA forms
-// the log-sum-exps of the head's group from the partial maxima and sums (a few hundred bytes); x = 0
-// writes out and lse, and each x the weights of its SLOTS slots.
+// the log-sum-exps of the head's group from the partial maxima and sums (a few hundred bytes), writes out and lse
+// of the query heads x, x + gridDim.x, .., and the weights of the SLOTS slots from x SLOTS on.
 constexpr int KEPT_FINISH_THREADS = 256, KEPT_FINISH_SLOTS = 1024;
-constexpr int KEPT_FACTORS = 1024;  // (head, range) factors held in shared memory at a time
 
 template <int D>
 __global__ void __launch_bounds__(KEPT_FINISH_THREADS) decode_kept_finish_kernel(const __grid_constant__ KeptArgs a) {
   __shared__ float s_lse2[kept::MAX_G];
-  __shared__ float s_f[KEPT_FACTORS];
   pdl_launch_dependents();
   pdl_wait();
   const int kvh = blockIdx.y, b = blockIdx.z, g = a.hq / a.hkv;
@@ -499,7 +497,7 @@ __global__ void __launch_bounds__(KEPT_FINISH_THREADS) decode_kept_finish_kernel
     return;
   }
   const int beg = blockIdx.x * KEPT_FINISH_SLOTS;
-  if (blockIdx.x > 0 && beg >= seq.n) return;
+  if (blockIdx.x >= g && beg >= seq.n) return;
   const int n_split = (seq.n + a.split_len - 1) / a.split_len;
   if (warp < g) {
     const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + (head0 + warp) * a.n_split;
@@ -520,53 +518,39 @@ __global__ void __launch_bounds__(KEPT_FINISH_THREADS) decode_kept_finish_kernel
     if (lane == 0) s_lse2[warp] = m + log2f(l);
   }
   __syncthreads();
-  if (blockIdx.x == 0) {
-    // out: four values a thread, the ranges dealt to the thread groups that share them
-    constexpr int Q = D / 4;                       // threads a head's row
-    const int rows_par = KEPT_FINISH_THREADS / Q;  // rows in flight, 8 at least: (head, slice of the ranges)
-    const int per = KEPT_FACTORS / kept::MAX_G;    // ranges a round
-    __shared__ float4 s_part[KEPT_FINISH_THREADS];
-    const int slices = max(1, rows_par / g);       // slices a head
-    const int rr = threadIdx.x / Q, d4 = threadIdx.x % Q;
-    const int h = rr % g, sl = rr / g;
-    const bool on = sl < slices && rr < g * slices;
-    {
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int r0 = 0; r0 < n_split; r0 += per) {
-        const int cnt = min(per, n_split - r0);
-        __syncthreads();
-        for (int i = threadIdx.x; i < g * cnt; i += KEPT_FINISH_THREADS) {
-          const int hh = i / cnt, sp = i % cnt;
-          s_f[hh * per + sp] = fast_exp2(a.part_ml[((head0 + hh) * a.n_split + r0 + sp) * 2] - s_lse2[hh]);
-        }
-        __syncthreads();
-        if (on) {
-          const float4* src = reinterpret_cast<const float4*>(a.part_o + ((head0 + h) * a.n_split + r0) * D) + d4;
+  // out: the CTAs of a (sequence, kv head) take its query heads in turn; four values a thread, the ranges dealt to
+  // the thread groups that share them, summed in a fixed order
+  constexpr int Q = D / 4;                         // threads a row
+  constexpr int SLICES = KEPT_FINISH_THREADS / Q;  // ranges in flight
+  __shared__ float4 s_part[KEPT_FINISH_THREADS];
+  const int sl = threadIdx.x / Q, d4 = threadIdx.x % Q;
+  for (int h = blockIdx.x; h < g; h += gridDim.x) {
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + (head0 + h) * a.n_split;
+    const float4* src = reinterpret_cast<const float4*>(a.part_o + (head0 + h) * a.n_split * D) + d4;
 #pragma unroll 4
-          for (int sp = sl; sp < cnt; sp += slices) {
-            const float4 x = src[static_cast<long long>(sp) * Q];
-            const float f = s_f[h * per + sp];
-            acc.x += x.x * f;
-            acc.y += x.y * f;
-            acc.z += x.z * f;
-            acc.w += x.w * f;
-          }
-        }
-      }
-      s_part[threadIdx.x] = acc;
-      __syncthreads();
-      if (on && sl == 0) {
-        for (int i = 1; i < slices; ++i) {
-          const float4 x = s_part[(i * g + h) * Q + d4];
-          acc.x += x.x;
-          acc.y += x.y;
-          acc.z += x.z;
-          acc.w += x.w;
-        }
-        *reinterpret_cast<uint2*>(a.out + (head0 + h) * D + 4 * d4) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-        if (a.lse && d4 == 0) a.lse[head0 + h] = s_lse2[h] * 0.69314718055994530942f;
-      }
+    for (int sp = sl; sp < n_split; sp += SLICES) {
+      const float4 x = src[static_cast<long long>(sp) * Q];
+      const float f = fast_exp2(ml[sp].x - s_lse2[h]);
+      acc.x += x.x * f;
+      acc.y += x.y * f;
+      acc.z += x.z * f;
+      acc.w += x.w * f;
     }
+    s_part[threadIdx.x] = acc;
+    __syncthreads();
+    if (sl == 0) {
+      for (int i = 1; i < SLICES; ++i) {
+        const float4 x = s_part[i * Q + d4];
+        acc.x += x.x;
+        acc.y += x.y;
+        acc.z += x.z;
+        acc.w += x.w;
+      }
+      *reinterpret_cast<uint2*>(a.out + (head0 + h) * D + 4 * d4) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+      if (a.lse && d4 == 0) a.lse[head0 + h] = s_lse2[h] * 0.69314718055994530942f;
+    }
+    __syncthreads();
   }
   if (!a.kweight) return;
   // four slots a thread in flight

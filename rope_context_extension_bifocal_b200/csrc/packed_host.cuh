@@ -310,7 +310,8 @@ cudaError_t launch_kept(const bf::KeptArgs& a, int batch, cudaStream_t st) {
                         : g <= 4 ? launch_kept_g<D, 4>(a, batch, st)
                                  : launch_kept_g<D, 8>(a, batch, st);
   if (e != cudaSuccess) return e;
-  const int64_t chunks = a.kweight ? (static_cast<int64_t>(a.max_len) + bf::KEPT_FINISH_SLOTS - 1) / bf::KEPT_FINISH_SLOTS : 1;
+  // a CTA a query head, and one every KEPT_FINISH_SLOTS slots whose weights are added
+  const int64_t chunks = std::max<int64_t>(g, a.kweight ? (static_cast<int64_t>(a.max_len) + bf::KEPT_FINISH_SLOTS - 1) / bf::KEPT_FINISH_SLOTS : 1);
   return launch_pdl(bf::decode_kept_finish_kernel<D>, dim3(static_cast<unsigned>(chunks), a.hkv, batch),
                     dim3(bf::KEPT_FINISH_THREADS), 0, st, a);
 }
