@@ -14,12 +14,15 @@
 // under position aliasing (angles as in turn_cos_sin).
 //
 // What bounds it: 4 D bytes of K and V a slot and kv head from HBM, and, next to that, instructions
-// (about 50 a slot and kv head and warp for four query heads at D = 128: half of them the sines and
+// (about 80 of a warp a slot and kv head for four query heads at D = 128; a fifth of them are sines and
 // cosines, which no table can share since every head has positions of its own). QK^T and PV run on
 // packed fp32 FMAs: with at most 8 query rows they cost less than the conversions and the split
 // operands that the tensor cores would need to keep scores, and so weights, exact to fp32.
+// Measured: 16 sequences of 640 to 8192 slots, 32 / 8 heads of 128 with weights (314 MB): 104 us and 13 us for the
+// merge, 2.8 TB/s of 6.55 with 59% of the issue slots busy; the same rows held in registers instead of a ring in
+// shared memory (8 warps an SM instead of 16) took 190 us.
 //
-// Work split: a CTA takes a range of slots of one (sequence, kv head), a warp every fourth chunk of
+// Work split: a CTA takes a range of slots of one (sequence, kv head), a warp every fourth block of 32 of
 // it; D / 8 lanes share a key (4 pairs each). A second kernel merges the ranges and adds the weights.
 // Padded to 1, 2, 4 or 8 query heads a kv head (GP).
 #pragma once

@@ -15,20 +15,23 @@
 // rounding shifts all its scores alike (the queries that attend to it lean its way), so its low part is always
 // needed: without it weights are 3e-5 off however many queries there are. The queries' roundings are independent
 // and average out: from ROUNDED_FROM (query, head) rows on Kh Ql is left out (a third of the tensor work and half the
-// query bytes), and weights are within 6e-6.
+// query bytes: all queries of 6001 tokens 340 us instead of 467), and weights are within 6e-6.
 //
 // Keys come raw from global memory and are turned by the softmax warps themselves, once for each branch
 // the tile has (the local queries first, then the long-range ones); no rotated copy of k is written. The
 // query rows are turned once by weights_query_kernel and arrive by TMA.
 //
-// Warp roles: the first 8 or 16 warps form the key tile and then sum (groups of four warps, one visit each in
-// turn; warp w reads TMEM lanes 32 (w % 4) ..), then a TMA producer and an MMA issuer. A visit is one
+// Warp roles: the first 8 or 16 warps form the key tile and then sum (groups of four warps: a visit each in turn, or a
+// quarter of every visit's columns; warp w reads TMEM lanes 32 (w % 4) ..), then a TMA producer and an MMA issuer. A visit is one
 // query tile under one branch. Shared memory holds the key tile (high and low part) and a ring of query tiles.
 //
 // Few rows (QT = 64): each key tile has a handful of visits and its time is the latency of forming it, so two
 // CTAs share an SM (96 KB and 256 tensor-memory columns each). Many rows (QT = 256): one CTA, two 64 KB query slots,
-// two S tiles of 256 columns, each summed by two groups; wide products, because what the issuing thread does between
+// two S tiles of 256 columns, each summed by four groups; wide products, because what the issuing thread does between
 // two visits is idle time of the tensor core (with 128 columns it was half of it).
+// Measured, 32 / 8 heads of 128: last 32 queries of 100003 tokens 194 us (keys alone 32 us at the copy rate; the 11 us
+// a key tile takes are the latency of its steps: load, turn, product, sum), all queries of 6001 tokens 338 us (the
+// two products 182 us at the tensor peak; tensor pipe 57% and ex2 unit 59% busy).
 #pragma once
 #include <type_traits>
 
@@ -74,7 +77,6 @@ struct WeightArgs {
   int hq, hkv;
   int window_pitch;   // queries set aside for a sequence in the forms; 0: as many as it has rows
   int w0, w_pretrained, mode, window;
-  int head_major;     // CTAs in the order of kv heads (their query forms share L2), or of work alone
   __half* forms[4];   // the forms above, as weights_query_kernel writes them: Qo high, low, Ql high, low
   float* nl;          // [hkv][nl_pitch] -lse * log2(e) of the rows of the forms
   int form_rows;      // queries of the forms (g rows each)
@@ -292,8 +294,9 @@ __global__ void __launch_bounds__(kw::threads<QT>(), QT == 64 ? 2 : 1) key_weigh
   pdl_launch_dependents();
   pdl_wait();
   const int idx = static_cast<int>(blockIdx.x);
-  const int kvh = a.head_major ? idx / a.plan.max_tiles : idx % a.hkv;
-  const int rank = a.head_major ? idx % a.plan.max_tiles : idx / a.hkv;
+  // heaviest tiles first over all heads (a head after the other, whose query forms would share L2, took 372 us
+  // instead of 340 at 6001 tokens and as long at 20000)
+  const int kvh = idx % a.hkv, rank = idx / a.hkv;
   const PackedTile tile = a.plan.tiles[rank];
   if (rank >= a.plan.head->n_tiles) return;
   const int g = a.hq / a.hkv;

@@ -212,6 +212,8 @@ __device__ __forceinline__ bool all_finite(__half2 top) {
   return f.x < INFINITY && f.y < INFINITY;  // false for a NaN
 }
 
+constexpr int kRopeRows = 2;  // rows a CTA (with eight, 4000 rows took 103 us in all instead of 96, 14188 the same)
+
 // What a CTA's warps need of each of its rows.
 struct RopeRow {
   int b, p, G;       // sequence (-1: none), position, factor
@@ -235,17 +237,18 @@ __device__ __forceinline__ void turn8(const V& x1, const V& x2, const float4 (&c
   }
 }
 
-// A CTA takes ROWS rows (the first CTA makes the tile list instead): it looks them up, evaluates their angles
+// A CTA takes two rows (the first CTA makes the tile list instead): it looks them up, evaluates their angles
 // once for all heads (fp64 product and reduction, see angle_cos_sin), then deals (row, four heads) units to its
 // warps, eight lanes a head and eight pairs a lane. A warp keeps UNITS loads in flight, the first ones while the
-// angles are formed. Memory bound: it reads q, k, v once and writes each form once. The long-range forms that no
+// angles are formed. Memory bound: it reads q, k, v once and writes each form once: 99 us for 14188 rows of 32 / 8
+// heads of 128 (480 MB: 4.8 TB/s of 6.55), 16 us for 1607 rows (latency). Token-major forms took the same time. The long-range forms that no
 // pair uses are left out: of queries in the 128 rows of an attention tile that ends before w0 (no key is that
 // far back), and of keys in a tile that no query of the sequence is w0 past.
-template <typename Tin, int D, int ROWS>
+template <typename Tin, int D>
 __global__ void __launch_bounds__(kPlanThreads, sizeof(Tin) == 2 ? 3 : 2) rope_packed_kernel(const __grid_constant__ PackedRopeArgs a) {
   constexpr int P = D / 2;
   constexpr int LPR = P / 8;  // lanes a head
-  constexpr int UNITS = 3;
+  constexpr int UNITS = 3, ROWS = kRopeRows;
   __shared__ RopeRow s_row[ROWS];
   __shared__ float4 s_cs[ROWS][2][4][LPR];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
