@@ -252,8 +252,8 @@ struct KeptLayout {
 };
 
 // Ranges of slots: about 1024 CTAs in all (seven of 128 threads on each SM) as long as a range keeps 64
-// slots, and never more than 512 slots in one, so that a batch of unequal lengths fills the GPU evenly (81K slots of 16
-// sequences: 115 us; ranges of up to 1024 slots 121 us, of 256 118 us, which also costs long caches 18%).
+// slots, and never more than 512 slots in one, so that a batch of unequal lengths fills the GPU evenly (75.6K slots of
+// 16 sequences: 115 us; ranges of up to 1024 slots 121 us, of 256 118 us, which also costs long caches 18%).
 KeptLayout kept_layout(int batch, int max_len, bool accumulate, const bf_params_t* p) {
   KeptLayout w{};
   const int64_t segs = static_cast<int64_t>(batch) * p->hkv;
@@ -339,7 +339,7 @@ bf_status_t decode_kept_impl(const void* q, const void* k_new, const void* v_new
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const Rope rope = make_rope(p->rope_theta, p->head_dim, 1);
   // A stage's slots share a page, and are one box of the pool, where pages hold whole stages; other page sizes are
-  // copied row by row (81K slots: 114 us with pages of 64, 135 us with pages of 12).
+  // copied row by row (75.6K slots: 114 us with pages of 64, 135 us with pages of 12).
   a.boxes = page_size % (bf::kept::STAGE_BYTES / (4 * p->head_dim)) == 0 ? 1 : 0;
   if (a.boxes && (!make_slot_map(&a.k_map, kcache, cache_rows, p->hkv, p->head_dim) ||
                   !make_slot_map(&a.v_map, vcache, cache_rows, p->hkv, p->head_dim)))
