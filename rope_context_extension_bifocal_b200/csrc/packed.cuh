@@ -212,7 +212,10 @@ __device__ __forceinline__ bool all_finite(__half2 top) {
   return f.x < INFINITY && f.y < INFINITY;  // false for a NaN
 }
 
-constexpr int kRopeRows = 2;  // rows a CTA (with eight, 4000 rows took 103 us in all instead of 96, 14188 the same)
+// Rows a CTA: with two, few heads leave a warp too little to keep its loads in flight (whole prefill of 3775 rows of
+// 12 / 4 fp32 heads of 64: 71 us instead of 65), with eight, few rows leave SMs idle (1607 rows of 32 / 8 heads of 128:
+// 48 us instead of 44); 14188 and 25012 rows take the same with either.
+constexpr int kRopeRows = 4;
 
 // What a CTA's warps need of each of its rows.
 struct RopeRow {
@@ -237,7 +240,7 @@ __device__ __forceinline__ void turn8(const V& x1, const V& x2, const float4 (&c
   }
 }
 
-// A CTA takes two rows (the first CTA makes the tile list instead): it looks them up, evaluates their angles
+// A CTA takes four rows (the first CTA makes the tile list instead): it looks them up, evaluates their angles
 // once for all heads (fp64 product and reduction, see angle_cos_sin), then deals (row, four heads) units to its
 // warps, eight lanes a head and eight pairs a lane. A warp keeps UNITS loads in flight, the first ones while the
 // angles are formed. Memory bound: it reads q, k, v once and writes each form once: 99 us for 14188 rows of 32 / 8
