@@ -29,7 +29,7 @@
 // CTAs share an SM (96 KB and 256 tensor-memory columns each). Many rows (QT = 256): one CTA, two 64 KB query slots,
 // two S tiles of 256 columns, each summed by four groups; wide products, because what the issuing thread does between
 // two visits is idle time of the tensor core (with 128 columns it was half of it).
-// Measured, 32 / 8 heads of 128: last 32 queries of 100003 tokens 194 us (keys alone 32 us at the copy rate; the 11 us
+// Measured, 32 / 8 heads of 128: last 32 queries of 100003 tokens 191 us (keys alone 32 us at the copy rate; the 11 us
 // a key tile takes are the latency of its steps: load, turn, product, sum), all queries of 6001 tokens 338 us (the
 // two products 182 us at the tensor peak; tensor pipe 57% and ex2 unit 59% busy).
 #pragma once
