@@ -29,7 +29,7 @@ namespace ev {
 constexpr int THREADS = 1024;
 constexpr int WARPS = THREADS / 32;
 constexpr int BINS = 2048;          // of a pass: 11 bits of the key
-constexpr int COPIES = 4;           // histograms a CTA fills side by side (fewer conflicts on one bin)
+constexpr int COPIES = 2;           // histograms a CTA fills side by side (fewer conflicts on one bin; four took the same time)
 constexpr int CTA_SLOTS = 16384;    // slots a CTA takes while a cluster of 8 suffices
 constexpr int MAX_RESIDENT = 40960; // keys a CTA holds in shared memory; longer ranges are read again each pass
 }  // namespace ev

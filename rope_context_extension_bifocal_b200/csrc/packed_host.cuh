@@ -142,7 +142,10 @@ bf_status_t prefill_packed_impl(const void* q, const void* k, const void* v, int
       !aligned(cu_seqlens, 4) || (lse && !aligned(lse, 4)))
     return BF_ERR_INVALID;
   const bool window = (p->flags & BF_FLAG_WINDOW) != 0;
-  const bool even = (p->hq / p->hkv) % 2 == 0;  // two heads of a group a CTA
+  // Even groups: two heads of a group a CTA, in the ping-pong kernel (whole call, 32 / 8 heads of 128: 64 prompts of 128
+  // rows 126 us, with the single-tile kernel 161; 4 of 1000 rows 97 and 110; one of 1000, too few CTAs for the GPU, 33
+  // and 31)
+  const bool even = (p->hq / p->hkv) % 2 == 0;
   if (window && !even) return BF_ERR_UNSUPPORTED;
   bf::CacheRows rows{};
   if (kcache || vcache || kpos) {
