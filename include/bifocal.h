@@ -325,10 +325,9 @@ BF_API bf_status_t bifocal_decode_paged(const void* q, const void* k_new, const 
  *          other places are left as they were
  *   workspace / ws_bytes: >= bifocal_key_weights_workspace_size(batch, total_rows, max_len, obs, p), 256-byte aligned
  *          (forms of the queries that count: four fp16 copies).
- * Scores are formed from operands split in two fp16 parts (about 2^-21 relative), not from the single fp16
- * operands of the prefill; from 16384 (query, head) rows a sequence on, the queries are single fp16 values, whose
- * roundings average out over so many. Errors on the device as for bifocal_prefill_packed; |q| or |k| from 65520 on is
- * reported as BF_ERR_RANGE. Flags: BF_FLAG_WINDOW drops the long-range pairs (any head_dim and group).
+ * Scores are formed from operands split in two fp16 parts, not from the single fp16 operands of the prefill: each
+ * element is held to 2^-22 of itself, or to 2^-25 where it is smaller than 2^-3. Errors on the device as for
+ * bifocal_prefill_packed; |q| or |k| from 65520 on is reported as BF_ERR_RANGE. Flags: BF_FLAG_WINDOW drops the long-range pairs (any head_dim and group).
  * Errors: as bifocal_prefill_packed; BF_ERR_INVALID also for NULL lse or kweight and obs < 1. */
 BF_API size_t bifocal_key_weights_workspace_size(int32_t batch, int32_t total_rows, int32_t max_len, int32_t obs,
                                                  const bf_params_t* p);

@@ -11,11 +11,11 @@
 //
 // Precision. A single fp16 rounding of the rotated operands moves a score by about 3e-4, and so a weight
 // summed from few queries by as much, relative. Each operand is therefore split into an fp16 value and the
-// fp16 rest, and S = Kh Qh + Kl Qh + Kh Ql (the term left out is 2^-22): scores exact to about 1e-6. A key's own
-// rounding shifts all its scores alike (the queries that attend to it lean its way), so its low part is always
-// needed: without it weights are 3e-5 off however many queries there are. The queries' roundings are independent
-// and average out: from ROUNDED_FROM (query, head) rows on Kh Ql is left out (a third of the tensor work and half the
-// query bytes: all queries of 6001 tokens 340 us instead of 467), and weights are within 6e-6.
+// fp16 rest, and S = Kh Qh + Kl Qh + Kh Ql (the term left out is 2^-22): scores exact to about 1e-6. Neither low part
+// can be spared, however long the sum: a key's own rounding shifts all its scores alike (the queries that attend to it
+// lean its way), and what averages out of the queries' roundings depends on how many queries carry a key's weight, one of
+// each head for the last key, a few under peaked scores. Without Kh Ql all queries of 6001 tokens took 340 us, and single
+// weights were 2e-4 off (1.5e-3 with queries four times the size).
 //
 // Keys come raw from global memory and are turned by the softmax warps themselves, once for each branch
 // the tile has (the local queries first, then the long-range ones); no rotated copy of k is written. The
@@ -30,8 +30,8 @@
 // two S tiles of 256 columns, each summed by four groups; wide products, because what the issuing thread does between
 // two visits is idle time of the tensor core (with 128 columns it was half of it).
 // Measured, 32 / 8 heads of 128: last 32 queries of 100003 tokens 191 us (keys alone 32 us at the copy rate; the 11 us
-// a key tile takes are the latency of its steps: load, turn, product, sum), all queries of 6001 tokens 338 us (the
-// two products 182 us at the tensor peak; tensor pipe 57% and ex2 unit 59% busy).
+// a key tile takes are the latency of its steps: load, turn, product, sum), all queries of 6001 tokens 466 us (the
+// three products 273 us at the tensor peak).
 #pragma once
 #include <type_traits>
 
@@ -46,7 +46,6 @@ namespace bf {
 namespace kw {
 constexpr int QROWS = 4;  // query rows a CTA of weights_query_kernel
 constexpr uint32_t HALF = 16384;    // 128 rows of 64 fp16 values
-constexpr int ROUNDED_FROM = 16384; // (query, head) rows from which the queries' low parts are left out
 constexpr int NSLOT = 2;            // query tiles in the ring
 constexpr int NROW = 4;             // rows of log-sum-exps in shared memory
 // S tiles in tensor memory; summing groups of four warps; groups that share a visit, each a range of its columns
@@ -132,7 +131,7 @@ __global__ void __launch_bounds__(kPlanThreads) weights_query_kernel(const __gri
   constexpr int LPR = P / 8;
   constexpr int UNITS = 2;
   struct Row {
-    int w, r, p, G, lng, low;  // query of the forms (-1: none), packed row, position, factor, forms wanted
+    int w, r, p, G, lng;  // query of the forms (-1: none), packed row, position, factor, long-range form wanted
   };
   __shared__ Row s_row[kw::QROWS];
   __shared__ float4 s_cs[kw::QROWS][2][4][LPR];
@@ -177,7 +176,6 @@ __global__ void __launch_bounds__(kPlanThreads) weights_query_kernel(const __gri
         x.r = first + x.p;
         x.G = factor_of(n, a.w_pretrained);
         x.lng = !a.window && has_long_pairs(n, x.G, a.w0);
-        x.low = static_cast<long long>(cnt) * g < kw::ROUNDED_FROM;
       }
     }
     s_row[threadIdx.x] = x;
@@ -231,10 +229,10 @@ __global__ void __launch_bounds__(kPlanThreads) weights_query_kernel(const __gri
         uint4 hi, lo;
         split_f16(y1, hi, lo, top);
         *reinterpret_cast<uint4*>(a.forms[2 * f] + at + k0) = hi;
-        if (x.low) *reinterpret_cast<uint4*>(a.forms[2 * f + 1] + at + k0) = lo;
+        *reinterpret_cast<uint4*>(a.forms[2 * f + 1] + at + k0) = lo;
         split_f16(y2, hi, lo, top);
         *reinterpret_cast<uint4*>(a.forms[2 * f] + at + P + k0) = hi;
-        if (x.low) *reinterpret_cast<uint4*>(a.forms[2 * f + 1] + at + P + k0) = lo;
+        *reinterpret_cast<uint4*>(a.forms[2 * f + 1] + at + P + k0) = lo;
       }
     }
   }
@@ -295,7 +293,7 @@ __global__ void __launch_bounds__(kw::threads<QT>(), QT == 64 ? 2 : 1) key_weigh
   pdl_wait();
   const int idx = static_cast<int>(blockIdx.x);
   // heaviest tiles first over all heads (a head after the other, whose query forms would share L2, took 372 us
-  // instead of 340 at 6001 tokens and as long at 20000)
+  // instead of 340 at 6001 tokens and as long at 20000, without the product of the queries' low part)
   const int kvh = idx % a.hkv, rank = idx / a.hkv;
   const PackedTile tile = a.plan.tiles[rank];
   if (rank >= a.plan.head->n_tiles) return;
@@ -308,8 +306,6 @@ __global__ void __launch_bounds__(kw::threads<QT>(), QT == 64 ? 2 : 1) key_weigh
   const int w0 = (a.window || lng_pairs) ? a.w0 : kAllLocal;
   const int rows = cnt * g;              // (query, head) rows
   const int qrow = first_query(a, tile.seq, tile.first) * g;  // their first row in the forms
-  const bool low = rows < ROUNDED_FROM;  // the queries' low parts count
-  const int fpv = low ? 2 : 1;           // ring fills a visit
   // Query tile t holds rows QT t .. QT t + QT - 1: queries start + QT t / g .. start + (QT t + QT - 1) / g. Tiles
   // [t_first, t_oe) have local pairs with these keys, tiles [t_lb, n_t) long-range ones; a tile in both is
   // visited under either branch.
@@ -392,8 +388,8 @@ __global__ void __launch_bounds__(kw::threads<QT>(), QT == 64 ? 2 : 1) key_weigh
         nl_used |= 1u << buf;
         nl_par ^= 1u << buf;
         bool ok = true;
-        for (int x = 0; x < fpv; ++x) {
-          const int n = fpv * v + x, slot = n % NSLOT;
+        for (int x = 0; x < 2; ++x) {
+          const int n = 2 * v + x, slot = n % NSLOT;
           if (n >= NSLOT && !mbar_wait_suspend(&q_empty[slot], (n / NSLOT - 1) & 1, 101, &s_abort)) {
             ok = false;
             break;
@@ -440,13 +436,11 @@ __global__ void __launch_bounds__(kw::threads<QT>(), QT == 64 ? 2 : 1) key_weigh
         product(d, dkl, bh, true);
         mma_commit(&q_empty[slot]);
         if (++slot == NSLOT) slot = 0, slot_ph ^= 1u;
-        if (low) {
-          if (!mbar_wait_abortable(&q_full[slot], slot_ph, 114, &s_abort)) break;
-          fence_after();
-          product(d, dkh, dq0 + static_cast<uint64_t>(slot * (QTILE >> 4)), true);
-          mma_commit(&q_empty[slot]);
-          if (++slot == NSLOT) slot = 0, slot_ph ^= 1u;
-        }
+        if (!mbar_wait_abortable(&q_full[slot], slot_ph, 114, &s_abort)) break;
+        fence_after();
+        product(d, dkh, dq0 + static_cast<uint64_t>(slot * (QTILE >> 4)), true);
+        mma_commit(&q_empty[slot]);
+        if (++slot == NSLOT) slot = 0, slot_ph ^= 1u;
         mma_commit(&s_full[buf]);
         if (v == n_o - 1 && n_l > 0) mma_commit(&k_free);
         if (++buf == NBUF) buf = 0, buf_ph ^= 1u;

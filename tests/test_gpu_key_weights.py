@@ -184,3 +184,45 @@ def test_bad_boundaries_and_pages_are_reported():
     bfl.bifocal_key_weights(q, k, lse, cu, 80, 10, kweight=out, page_size=32, block_table=table, **kw)
     assert bfl.last_device_error() == bfl.STATUS_INDEX
     assert torch.equal(out[:, 32:64], want[:, :32]) and torch.equal(out[:, :16], want[:, 64:]) and torch.all(out[:, 64:] == -3)
+
+
+LONG = [
+    # lens (of several, some have more than 16384 (query, head) rows and some fewer), hq, hkv, D, dtype, w0, w_pretrained, mode, q's size
+    ([2100, 300], 8, 1, 128, torch.bfloat16, 300, 700, si.FREQ_INTERP, 1),
+    ([2100], 8, 1, 128, torch.bfloat16, 300, 700, si.FREQ_INTERP, 4),
+    ([150, 2070], 8, 1, 128, torch.float32, 0, 500, si.POS_ALIAS, 3),
+    ([2100, 1], 8, 1, 64, torch.bfloat16, 1000, 300, si.POS_ALIAS, 3),
+    ([2064], 16, 2, 64, torch.float32, 513, 1000, si.FREQ_INTERP, 1),
+    ([700, 129], 6, 2, 128, torch.float32, 200, 300, si.FREQ_INTERP, 1),
+]
+
+
+@pytest.mark.parametrize("case", range(len(LONG)))
+def test_every_key_over_all_queries(case):
+    """Every single weight over all queries of long prompts is as exact as over few: the last keys too, which few
+    queries see, and under peaked scores (q of three and four times the size). To the tolerance above comes the rounding of
+    -lse log2(e), 2^-23 of it, which larger scores make larger than 1e-6."""
+    lens, hq, hkv, D, dtype, w0, wp, mode, big = LONG[case]
+    g = si.generator(700 + case)
+    T = sum(lens)
+    q, k = ((big if h == hq else 1) * torch.randn(T, h, D, generator=g) for h in (hq, hkv))
+    q, k = q.to(dtype), k.to(dtype)
+    cu = [sum(lens[:i]) for i in range(len(lens) + 1)]
+    lse, want, tol = torch.empty(hq, T), [], []
+    for b, n in enumerate(lens):
+        s = slice(cu[b], cu[b] + n)
+        x, size = scores(q[s].double().numpy(), k[s].double().numpy(), w0, wp, mode, False)
+        m = x.max(2)
+        l = (m + np.log(np.exp(x - m[..., None]).sum(2))).astype(np.float32)
+        lse[:, s] = torch.from_numpy(l)
+        x -= l[..., None].astype(np.float64)
+        want.append(np.exp(x, out=x).sum(1).reshape(hkv, hq // hkv, n).sum(1))
+        tol.append(EPS * size + 4e-6 + 2.0 ** -23 * np.abs(l).max())
+    got = bfl.bifocal_key_weights(q.cuda(), k.cuda(), lse.cuda(), torch.tensor(cu, dtype=torch.int32).cuda(), max(lens),
+                                  max(lens), w0=w0, w_pretrained=wp, theta=THETA, mode=mode)
+    assert bfl.last_device_error() == 0
+    got = got.cpu().double().numpy()
+    for b, n in enumerate(lens):
+        rel = np.abs(got[:, cu[b]:cu[b] + n] - want[b]) / np.maximum(want[b], 1e-30)
+        worst = int(rel.max(0).argmax())
+        assert np.all(rel * want[b] <= tol[b] * want[b] + 1e-30), (b, n, worst, rel.max(), tol[b])
