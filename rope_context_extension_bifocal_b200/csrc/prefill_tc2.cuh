@@ -617,6 +617,10 @@ __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __gri
     const uint32_t s_col = lane_addr + (x == 0 ? COL_SA : COL_SB);
     const uint32_t o_col = lane_addr + (x == 0 ? COL_OA : COL_OB);
     const float sc = a.scale_log2;
+    // Packed: rows of the tile past the sequence's end hold another sequence's queries or what the workspace held. In
+    // the warp's choices of a path below they count as the rows of zeros that the unpacked form has there, so that the
+    // sequence's own rows are those it gives alone, bit for bit.
+    const bool live = !PACKED || i < L;
     float m_ref = -INFINITY, l_sum = 0.f;
     bool ok = true;
     for (int v = 0; v < nv && ok; ++v) {
@@ -678,7 +682,7 @@ __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __gri
           return ((r8[0] + r8[1]) + (r8[2] + r8[3])) + ((r8[4] + r8[5]) + (r8[6] + r8[7]));
         };
         const float rs_lo = half_pass(0, f2_pack(-m_ref, -m_ref));
-        exact = __any_sync(0xffffffffu, !(rs_lo <= 16777216.f));
+        exact = __any_sync(0xffffffffu, live && !(rs_lo <= 16777216.f));
         if (!exact) {
           // send the first half: P over columns 0-31 of the S buffer (S of keys 0-63 is consumed)
           tmem_st32(s_col, pk);
@@ -689,7 +693,7 @@ __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __gri
           lo_sent = true;
           float rs_hi = half_pass(64, f2_pack(-m_ref, -m_ref));
           rs = rs_lo + rs_hi;
-          if (__any_sync(0xffffffffu, !(rs_hi <= 16777216.f))) {
+          if (__any_sync(0xffffffffu, live && !(rs_hi <= 16777216.f))) {
             // Rare: the second half's terms outgrow the reference the first half was sent with.
             // Its S columns (64-127) are intact: take the raw max over them, move the reference
             // where it grew past the threshold, and recompute the second half against it.
@@ -709,7 +713,7 @@ __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __gri
             const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
                                    fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) *
                              sc;
-            if (mx > m_ref + RESCALE_THRESHOLD) {
+            if (live && mx > m_ref + RESCALE_THRESHOLD) {
               alpha = fast_exp2(m_ref - mx);
               grow = true;
               m_ref = mx;
@@ -763,9 +767,10 @@ __global__ void __launch_bounds__(tc2::NTHREADS2, 1) attn_tc2_kernel(const __gri
 #pragma unroll
             for (int u = 0; u < 8; ++u) m8[u] = fmaxf(m8[u], s[c + u]);
         }
-        const float mx =
+        float mx =
             fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) *
             sc;
+        if (!live) mx = !masked || (i - j0 >= lo && i - j0 - (BN - 1) < hi) ? 0.f : -INFINITY;  // a score of 0 per key in range
         // lazy rescale: a row keeps its reference unless its max grew by more than the threshold
         if (mx > m_ref + RESCALE_THRESHOLD || (m_ref == -INFINITY && mx > -INFINITY)) {
           alpha = (m_ref == -INFINITY) ? 0.f : fast_exp2(m_ref - mx);

@@ -205,3 +205,28 @@ def test_bad_page_is_reported():
     assert bfl.last_device_error() == bfl.STATUS_INDEX
     assert torch.all(vc[64:] == 7) and torch.equal(vc[:32], x[2][:32].cuda()) and torch.equal(vc[32:64], x[2][64:96].cuda())
     check([100], x, cu, out, lse, 40, 64, si.FREQ_INTERP)
+
+
+@pytest.mark.parametrize("fill", [0x00, 0xff])
+@pytest.mark.parametrize("hq,hkv,D,window,w0,wp", [(4, 2, 128, False, 128, 512), (4, 2, 64, False, 128, 512), (3, 1, 128, False, 128, 512),
+                                                   (4, 2, 128, True, 300, 512), (8, 2, 128, False, 700, 900)])
+def test_rows_past_a_sequence_change_no_bit(hq, hkv, D, window, w0, wp, fill):
+    """The last query tile of a sequence of nine tiles and several unmasked ones holds rows of the next sequence: of one
+    without long-range forms (whatever the workspace held there: zeros, or NaN), of one whose scores outgrow any
+    reference. The results are those of the sequence alone, and of bifocal_prefill where it has the same kernel, bit for bit."""
+    lens = [1100, 200, 1061, 600]
+    x, cu = make(lens, hq, hkv, D, torch.bfloat16, 15)
+    x[0][cu[3]:] *= 64
+    kw = dict(w0=w0, w_pretrained=wp, theta=THETA, flags=bfl.FLAG_WINDOW if window else 0)
+    p = bfl.make_params(hq, hkv, D, w0, wp, THETA)
+    ws = torch.full((bfl.prefill_packed_workspace_size(bfl.DTYPE_BF16, 4, sum(lens), p),), fill, dtype=torch.uint8, device="cuda")
+    out, lse = bfl.bifocal_prefill_packed(*(t.cuda() for t in x), cu.cuda(), 1100, workspace=ws, **kw)
+    assert bfl.last_device_error() == 0
+    for b in (0, 2):
+        s = slice(int(cu[b]), int(cu[b + 1]))
+        one = [t[s].contiguous().cuda() for t in x]
+        alone, alone_lse = bfl.bifocal_prefill_packed(*one, torch.tensor([0, lens[b]], dtype=torch.int32).cuda(), 1100, **kw)
+        assert torch.equal(out[s], alone) and torch.equal(lse[:, s], alone_lse), b
+        if D == 128:
+            dense, dense_lse, _, _ = bfl.bifocal_prefill(*(t[None] for t in one), **kw)
+            assert torch.equal(out[s], dense[0]) and torch.equal(lse[:, s], dense_lse[0]), b
