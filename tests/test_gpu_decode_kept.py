@@ -212,3 +212,22 @@ def test_captured_replayed_and_on_another_stream():
         d, out, lse = call(s, d, **kw)
     side.synchronize()
     assert torch.equal(out, out0) and torch.equal(d["kw"].view(torch.int32), want["kw"].view(torch.int32))
+
+
+def test_position_zero_is_not_turned():
+    """The key of position 0 turned by the angle of position 0, and a query whose long-range angle is 0 (position 1, G = 2,
+    position aliasing): products of x with y halves alone, so the score is 0 whatever its operands' size. The new key is
+    0 as well: both probabilities are 1/2, the log-sum-exp is log 2."""
+    page, D, hkv, hq = 16, 128, 2, 8
+    kc, vc = torch.zeros(16, hkv, D, dtype=torch.bfloat16), torch.zeros(16, hkv, D, dtype=torch.bfloat16)
+    kc[0, :, :64], vc[0] = 256, 3
+    q, kn = torch.zeros(1, hq, D, dtype=torch.bfloat16), torch.zeros(1, hkv, D, dtype=torch.bfloat16)
+    q[..., 64:] = 256
+    kpos, kw = torch.zeros(hkv, 16, dtype=torch.int32).cuda(), torch.zeros(hkv, 16).cuda()
+    one = torch.tensor([1], dtype=torch.int32).cuda()
+    out, lse = bfl.bifocal_decode_kept(q.cuda(), kn.cuda(), kn.cuda(), kc.cuda(), vc.cuda(), kpos, kw, page,
+                                       torch.zeros(1, 1, dtype=torch.int32).cuda(), one + 1, one, 2, w0=1, w_pretrained=1,
+                                       theta=THETA, mode=si.POS_ALIAS)
+    assert bfl.last_device_error() == 0
+    assert (lse - np.log(2)).abs().max() <= 1e-6 * (1 + np.log(2))
+    assert (kw[:, :2] - hq / hkv / 2).abs().max() <= 2e-6 * hq / hkv / 2 and torch.all(out == 1.5)
