@@ -272,14 +272,14 @@ __global__ void __launch_bounds__(kept::WARPS * 32, GP <= 4 ? 4 : 2) decode_kept
       const unsigned rows_here = (row_mask >> (sub * CH)) & ((1u << CH) - 1u);
       const bool append = sbase + CH >= seq.n;
       if (rows_here != (1u << CH) - 1u || append) {
-        // Rare: rows past the range or of a bad page are zeroed, and the new token's row is written: its key
-        // rotated and rounded to the cache's bf16, so that this step uses it as every later one will.
+        // Rare: rows past the range or of a bad page are zeroed, and the new token's row is written (unless its
+        // page is bad): its key rotated and rounded to the cache's bf16, so that this step uses it as every later one will.
         for (int i = 0; i < CH; ++i)
           if (!((rows_here >> i) & 1u) && lane < 2 * LPK)
             *reinterpret_cast<uint4*>(st + (lane < LPK ? 0 : STAGE_BYTES / 2) + i * (2 * D) + (lane % LPK) * 16) = make_uint4(0u, 0u, 0u, 0u);
         __syncwarp();
-        const int i = seq.n - 1 - sbase;
-        if (i >= 0 && i < CH && lane < LPK) {
+        const int i = seq.n - 1 - sbase, new_row = __shfl_sync(0xffffffffu, row, (sub * CH + i) & 31);
+        if (i >= 0 && i < CH && new_row >= 0 && lane < LPK) {
           const long long src = (static_cast<long long>(b) * a.hkv + kvh) * D;
           const uint2 u = *reinterpret_cast<const uint2*>(a.k_new + src + 4 * ll);
           const uint2 w = *reinterpret_cast<const uint2*>(a.k_new + src + P + 4 * ll);
@@ -299,15 +299,11 @@ __global__ void __launch_bounds__(kept::WARPS * 32, GP <= 4 ? 4 : 2) decode_kept
           *reinterpret_cast<uint2*>(st + i * (2 * D) + ll * 8) = kx;
           *reinterpret_cast<uint2*>(st + i * (2 * D) + D + ll * 8) = ky;
           *reinterpret_cast<uint4*>(st + STAGE_BYTES / 2 + i * (2 * D) + ll * 16) = v;
-          const int page = (seq.n - 1) / a.rows.page_size, pg = trow[page];
-          if (pg >= 0 && pg < a.rows.pool_pages) {
-            const long long r = static_cast<long long>(pg) * a.rows.page_size + (seq.n - 1 - page * a.rows.page_size);
-            const long long at = (r * a.hkv + kvh) * D;
-            *reinterpret_cast<uint2*>(a.kcache + at + 4 * ll) = kx;
-            *reinterpret_cast<uint2*>(a.kcache + at + P + 4 * ll) = ky;
-            *reinterpret_cast<uint4*>(a.vcache + at + 8 * ll) = v;
-            if (ll == 0) a.kpos[static_cast<long long>(kvh) * a.rows.rows + r] = seq.now;
-          }
+          const long long at = (static_cast<long long>(new_row) * a.hkv + kvh) * D;
+          *reinterpret_cast<uint2*>(a.kcache + at + 4 * ll) = kx;
+          *reinterpret_cast<uint2*>(a.kcache + at + P + 4 * ll) = ky;
+          *reinterpret_cast<uint4*>(a.vcache + at + 8 * ll) = v;
+          if (ll == 0) a.kpos[static_cast<long long>(kvh) * a.rows.rows + new_row] = seq.now;
         }
         fence_proxy_async_smem();  // before the copy that will overwrite the stage
         __syncwarp();

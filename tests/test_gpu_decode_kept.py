@@ -231,3 +231,41 @@ def test_position_zero_is_not_turned():
     assert bfl.last_device_error() == 0
     assert (lse - np.log(2)).abs().max() <= 1e-6 * (1 + np.log(2))
     assert (kw[:, :2] - hq / hkv / 2).abs().max() <= 2e-6 * hq / hkv / 2 and torch.all(out == 1.5)
+
+
+def test_keys_and_values_of_a_bad_page_read_as_zeros():
+    """The page of the new token's slot, and one in the middle: the results are those of zero keys and values there (a
+    score of 0, whatever the position), the new token's among them, and nothing of these slots is written."""
+    s = make([60, 50, 40], 4, 2, 128, 16, 21)
+    kw = dict(w0=20, w_pretrained=64)
+    d = {k: (v.cuda() if torch.is_tensor(v) else v) for k, v in s.items()}
+    bad = {0: slice(48, 60), 1: slice(0, 0), 2: slice(16, 32)}
+    d["table"] = d["table"].clone()
+    d["table"][0, 3], d["table"][2, 1] = 999, -1
+    d, out, lse = call(s, d, **kw)
+    assert bfl.last_device_error() == bfl.STATUS_INDEX
+    out, lse, weight = (t.cpu().double().numpy() for t in (out, lse, d["kw"]))
+    for b, n in enumerate(s["lens"]):
+        r = rows_of(s["table"], 16, b, n)
+        now = int(s["now"][b])
+        good = np.ones(n, dtype=bool)
+        good[bad[b]] = False
+        for h in range(2):
+            q = s["q"][b, 2 * h:2 * h + 2].double().numpy()
+            keys, vals = d["kc"].cpu()[r, h].double().numpy(), d["vc"].cpu()[r, h].double().numpy()
+            keys[~good], vals[~good] = 0, 0
+            pos = d["kpos"].cpu()[h, r].numpy().copy()
+            pos[~good] = 0
+            ro, rl, w, pv = decode_kept(q, keys, vals, pos, now, 20, 64, si.FREQ_INTERP)
+            dlt = EPS / np.sqrt(128) * np.linalg.norm(q, axis=1) * np.linalg.norm(keys, axis=1).max()
+            rel = (2 * dlt + 2e-6)[:, None]
+            assert np.all(np.abs(out[b, 2 * h:2 * h + 2] - ro) <= 2.0 ** -8 * np.abs(ro) + rel * pv + 1e-30), (b, h)
+            assert np.all(np.abs(lse[b, 2 * h:2 * h + 2] - rl) <= dlt + 1e-6 * (1 + np.abs(rl))), (b, h)
+            old = s["kw"][h, r].double().numpy()
+            old[-1] = 0
+            err = np.abs(weight[h, r] - old - w)[good]
+            assert np.all(err <= (rel.max() * w + 2.0 ** -23 * (old + w))[good]), (b, h)
+            same = d["kw"].cpu()[h, r[~good]].view(torch.int32), s["kw"][h, r[~good]].view(torch.int32)
+            assert torch.equal(*same) and torch.equal(d["kpos"].cpu()[h, r[~good]], s["kpos"][h, r[~good]])
+        assert torch.equal(d["kc"].cpu()[r[~good]].view(torch.int16), s["kc"][r[~good]].view(torch.int16))
+        assert torch.equal(d["vc"].cpu()[r[~good]].view(torch.int16), s["vc"][r[~good]].view(torch.int16))
