@@ -180,3 +180,76 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         assert seq.tolist() == [256, 256]
         assert all(same(dev[x].cpu(), w) for x, w in zip(("kc", "vc", "kpos", "kw"), want))
+
+
+CLUSTERS = [
+    # lens, max_len (a CTA for every 16384 slots of it, up to eight), page, budget, recent, sink, weights
+    ([20000, 300, 16384], 20000, 64, 3000, 100, 4, "ties"),         # two CTAs a segment
+    ([33000, 1, 0, 32], 33000, 16, 9000, 0, 2, "special"),          # four
+    ([50001, 17000], 50001, 48, 17000, 1000, 0, "ties"),
+    ([66000, 40000], 66000, 128, 20000, 64, 16, "equal"),           # eight
+    ([140000], 140000, 64, 70001, 500, 4, "ties"),
+    ([70007], 100000, 64, 33, 16, 1, "special"),
+    ([5, 700, 4097, 90], 140000, 64, 300, 20, 4, "ties"),           # a bound far above the lengths: most CTAs have no slot
+]
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("case", range(len(CLUSTERS)))
+def test_segments_of_several_ctas_with_their_keys_resident(case, in_place):
+    """Two, four and eight CTAs a segment, each with its keys in shared memory, with ties and special values across their
+    borders: bit for bit a stable sort's choice."""
+    lens, max_len, page, budget, recent, sink, kind = CLUSTERS[case]
+    hkv, D = 2, 64
+    g = si.generator(80 + case)
+    table, pages = page_table(lens, page, g)
+    width = -(-max_len // page)
+    table = torch.cat([table, torch.full((len(lens), max(0, width - table.shape[1])), -1, dtype=torch.int32)], 1)
+    to_table, rows = table, pages * page
+    if not in_place:
+        to_table, more = page_table([min(n, budget) for n in lens], page, g)
+        to_table = torch.cat([to_table, torch.full((len(lens), -(-budget // page) - to_table.shape[1]), -1, dtype=torch.int32)], 1)
+        to_table = torch.where(to_table >= 0, to_table + pages, to_table)
+        rows += more * page
+    words = torch.arange(rows * hkv, dtype=torch.int32).view(rows, hkv, 1)  # each row its own contents
+    kc = words.repeat(1, 1, D // 2).view(torch.bfloat16).clone()
+    vc = (~words).repeat(1, 1, D // 2).view(torch.bfloat16).clone()
+    kpos, kw = torch.full((hkv, rows), -7, dtype=torch.int32), torch.full((hkv, rows), float("nan"))
+    special = torch.tensor([0.0, -0.0, float("inf"), -float("inf"), float("nan"), 1e-45, 3e38, -1.0, 1.0, 1.0000001])
+    newest = torch.tensor([2 * n + 3 for n in lens], dtype=torch.int32)
+
+    def at(t, b, n):
+        slot = torch.arange(n)
+        return t[b, slot // page].long() * page + slot % page
+
+    want = None
+    for b, n in enumerate(lens):
+        for h in range(hkv):
+            kpos[h, at(table, b, n)] = torch.randperm(2 * n + 4, generator=g)[:n].int()
+            kw[h, at(table, b, n)] = {"ties": lambda: torch.randint(0, 3, (n,), generator=g).float(), "equal": lambda: torch.zeros(n),
+                                      "special": lambda: special[torch.randint(0, len(special), (n,), generator=g)]}[kind]()
+    want = [t.clone() for t in (kc, vc, kpos, kw)]
+    for b, n in enumerate(lens):
+        m, src, dst = min(n, budget), at(table, b, n), at(to_table, b, min(n, budget))
+        for h in range(hkv):
+            pos, w = kpos[h, src], kw[h, src]
+            key = w.double().nan_to_num(nan=-np.inf, posinf=1e300, neginf=-np.inf)
+            key[(pos < sink) | (pos > int(newest[b]) - recent)] = np.inf
+            kept = torch.argsort(key, descending=True, stable=True)[:m].sort()[0]
+            if in_place:
+                hole = torch.ones(m, dtype=torch.bool)
+                hole[kept[kept < m]] = False
+                f, t = src[kept[kept >= m]], src[:m][hole]
+            else:
+                f, t = src[kept], dst
+            for new, old in zip(want[:2], (kc, vc)):
+                new[t, h] = old[f, h]
+            for new, old in zip(want[2:], (kpos, kw)):
+                new[h, t] = old[h, f]
+    dev = [t.cuda() for t in (kc, vc, kpos, kw)]
+    seq = torch.tensor(lens, dtype=torch.int32).cuda()
+    new = bfl.bifocal_cache_evict(*dev, page, table.cuda(), seq, newest.cuda(), max_len, budget, recent=recent, sink=sink,
+                                  dst_block_table=None if in_place else to_table.cuda())
+    assert bfl.last_device_error() == 0 and new.tolist() == [min(n, budget) for n in lens]
+    for got, ref, name in zip(dev, want, ("kcache", "vcache", "kpos", "kweight")):
+        assert same(got.cpu(), ref), name
