@@ -420,10 +420,12 @@ def _current_stream(device) -> int:
 
 class _On:
     """A call's stream (default: the current one of its tensors' device), made current with its device while the call
-    allocates and launches, so that what it allocates belongs to that stream."""
+    allocates and launches, so that what it allocates belongs to that stream. A stream of another device is refused."""
     __slots__ = ("device", "stream", "guards")
 
-    def __init__(self, device, stream):
+    def __init__(self, device, stream, where: str):
+        if stream is not None and stream.device != device:
+            raise BifocalError(1, f"{where}: the stream is on {stream.device}, the tensors on {device}")
         self.device, self.stream, self.guards = device, stream, ()
 
     def __enter__(self):
@@ -486,7 +488,7 @@ def bifocal_prefill_packed(q, k, v, cu_seqlens, max_len: int, *, w0: int, w_pret
                     ("workspace", workspace, None, None))
     p, pref = _cached_params(hq, hkv, D, int(w0), int(w_pretrained), float(theta), mode,
                              None if scale is None else float(scale), int(flags))
-    with _On(dev, stream) as st:
+    with _On(dev, stream, fn) as st:
         out = torch.empty(T, hq, D, dtype=bf16, device=dev) if out is None else out
         lse = torch.empty(hq, T, dtype=torch.float32, device=dev) if want_lse else None
         ws = _workspace(prefill_packed_workspace_size(dt, B, T, p), dev) if workspace is None else workspace
@@ -525,7 +527,7 @@ def bifocal_key_weights(q, k, lse, cu_seqlens, max_len: int, obs: int, *, w0: in
     obs = min(int(obs), int(max_len))
     p, pref = _cached_params(hq, hkv, D, int(w0), int(w_pretrained), float(theta), mode,
                              None if scale is None else float(scale), int(flags))
-    with _On(dev, stream) as st:
+    with _On(dev, stream, fn) as st:
         kweight = torch.empty(hkv, T, dtype=torch.float32, device=dev) if kweight is None else kweight
         ws = _workspace(key_weights_workspace_size(B, T, max_len, obs, p), dev) if workspace is None else workspace
         _check(_lib().bifocal_key_weights(
@@ -559,7 +561,7 @@ def bifocal_cache_evict(kcache, vcache, kpos, kweight, page_size: int, block_tab
                     ("block_table", block_table, (B, -1), i32), ("seq_lens", seq_lens, (B,), i32),
                     ("positions", positions, (B,), i32), ("dst_block_table", dst_block_table, (B, -1), i32),
                     ("new_lens", new_lens, (B,), i32), ("workspace", workspace, None, None))
-    with _On(dev, stream) as st:
+    with _On(dev, stream, fn) as st:
         new_lens = torch.empty_like(seq_lens) if new_lens is None else new_lens
         ws = _workspace(_cached_size(cache_evict_workspace_size, B, hkv, int(max_len), int(budget)), dev) if workspace is None else workspace
         _check(_lib().bifocal_cache_evict(
@@ -601,7 +603,7 @@ def bifocal_decode_kept(q, k_new, v_new, kcache, vcache, kpos, kweight, page_siz
                     ("workspace", workspace, None, None))
     p, pref = _cached_params(hq, hkv, D, int(w0), int(w_pretrained), float(theta), mode,
                              None if scale is None else float(scale), int(flags))
-    with _On(dev, stream) as st:
+    with _On(dev, stream, fn) as st:
         out = torch.empty(B, hq, D, dtype=bf16, device=dev) if out is None else out
         lse = torch.empty(B, hq, dtype=torch.float32, device=dev) if want_lse else None
         ws = workspace

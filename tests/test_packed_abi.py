@@ -125,3 +125,14 @@ def test_key_weights_validation(lib):
     small = bfl.key_weights_workspace_size(3, 1000, 600, 16, params())
     assert 0 < small < bfl.key_weights_workspace_size(3, 1000, 600, 600, params())
     assert bfl.key_weights_workspace_size(3, 1000, 600, 0, params()) == 0
+
+
+def test_binding_refuses_a_stream_of_another_device():
+    """Its kernels would run on that device, over pointers of another one."""
+    class Stream:
+        device = torch.device("cuda", 1)
+    with pytest.raises(bfl.BifocalError) as e:
+        bfl._On(torch.device("cuda", 0), Stream(), "bifocal_decode_kept")
+    assert e.value.status == INVALID and "bifocal_decode_kept" in str(e.value)
+    assert bfl._On(torch.device("cuda", 1), Stream(), "bifocal_decode_kept").stream is not None
+    assert bfl._On(torch.device("cuda", 0), None, "bifocal_decode_kept").stream is None
