@@ -38,9 +38,9 @@ FALLBACK_PEAKS = {"hbm_gbs": 6650.0, "bf16_tflops": 1590.0, "bf16_tflops_sustain
 # kernel has changed since the counters were taken and traffic is null.
 TRAFFIC = {
     "prefill_attention": {
-        "bytes_per_launch": 4.96e9 + 1.07e9,
+        "bytes_per_launch": 4.97e9 + 1.07e9,
         "sources": ["common.cuh", "prefill_tc.cuh", "prefill_tc2.cuh", "rope_loads.cuh"],
-        "sha256": "1acd80abf46fb7b2f676ab6d017fb4d89b6836e24c94c266b0675c9905212f45",
+        "sha256": "2be2b0b253ad50342c24976076a0f1dae79c380cb07e773d03ac7ecd65b7c398",
     },
 }
 

@@ -230,7 +230,8 @@ BF_API bf_status_t bifocal_prefill_chunk_paged(const void* q, const void* k, con
 
 /* Causal prefill of a packed batch: sequences of different lengths laid one after another, each with
  * its own positions from 0 and its own G = max(1, ceil(L_b / w_pretrained)). Rows see only rows of
- * their own sequence: sequence b's results are those of bifocal_prefill on its rows alone.
+ * their own sequence: sequence b's results are those of bifocal_prefill on its rows alone, and do not depend on
+ * the other rows of the call in any bit.
  *   q    [total_rows, hq,  D] raw, dtype;  k, v [total_rows, hkv, D] raw, dtype
  *   cu_seqlens [batch + 1] int32 (device): sequence b is rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1; a
  *          sequence may be empty; rows before cu_seqlens[0] and from cu_seqlens[batch] on belong to none:
@@ -240,7 +241,8 @@ BF_API bf_status_t bifocal_prefill_chunk_paged(const void* q, const void* k, con
  *   kcache, vcache [cache_rows, hkv, D] bf16 (both or neither): every key under the ORIGINAL RoPE and its
  *          value, at its packed row (block_table NULL; cache_rows >= total_rows), or at row
  *          block_table[b * max_pages + j / page_size] * page_size + j % page_size for key j of sequence b
- *          (cache_rows = pages * page_size, max_pages * page_size >= max_len, any page_size >= 1)
+ *          (cache_rows = pages * page_size, max_pages * page_size >= max_len, any page_size >= 1). Sequences may
+ *          share pages only where they hold the same keys and values at the same positions (a common prefix)
  *   kpos [hkv, cache_rows] int32 (may be NULL; needs the caches): the position of each key written, per
  *          kv head, as bifocal_cache_evict and bifocal_decode_kept read it
  *   workspace / ws_bytes: >= bifocal_prefill_packed_workspace_size(dtype, batch, total_rows, p), 256-byte
@@ -248,7 +250,9 @@ BF_API bf_status_t bifocal_prefill_chunk_paged(const void* q, const void* k, con
  * Boundaries that are not in order, exceed total_rows or give a length above max_len are reported as
  * BF_ERR_INDEX by bifocal_last_device_error, and nothing is written. A block-table entry outside the
  * pool is reported likewise and its rows are not written; the attention does not read the cache.
- * Both head sizes run on the tcgen05 kernels (two heads of a group a CTA, or one where the group is odd).
+ * Both head sizes run on the tcgen05 kernels (two heads of a group a CTA, or one where the group is odd), with
+ * bifocal_prefill's roundings for either input type: rotated queries and keys to fp16, values and probabilities to
+ * bf16; sums and statistics are fp32.
  * Flags: BF_FLAG_WINDOW as for bifocal_prefill, with an even group and either head_dim; BF_FLAG_FORCE_BIFOCAL
  * and BF_FLAG_FUSED_ROPE change nothing.
  * Errors: as bifocal_prefill; BF_ERR_INVALID also for NULL cu_seqlens, total_rows or max_len < 1 and bad
@@ -322,7 +326,8 @@ BF_API bf_status_t bifocal_decode_paged(const void* q, const void* k_new, const 
  *   obs  >= 1
  *   kweight [hkv, cache_rows] fp32, written (not added to): at the packed rows (block_table NULL;
  *          cache_rows >= total_rows) or at the rows the block table gives, as for bifocal_prefill_packed;
- *          other places are left as they were
+ *          other places are left as they were. No page may appear twice among the rows written: the weights
+ *          that sequences give to a page they share differ
  *   workspace / ws_bytes: >= bifocal_key_weights_workspace_size(batch, total_rows, max_len, obs, p), 256-byte aligned
  *          (forms of the queries that count: four fp16 copies).
  * Scores are formed from operands split in two fp16 parts, not from the single fp16 operands of the prefill: each

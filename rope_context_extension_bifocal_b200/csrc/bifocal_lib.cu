@@ -1226,8 +1226,8 @@ int32_t bifocal_device_status_word(void) {
 }
 
 const char* bifocal_build_info(void) {
-  return "bifocal sm_100a: rope pass; prefill D=128 tcgen05/TMEM/TMA (D=64 and BF_FLAG_MMA_SYNC: mma.sync); "
-         "decode split-KV (TMA + mma.sync)";
+  return "bifocal sm_100a: rope pass; prefill D=128 and packed prompts tcgen05/TMEM/TMA (other D=64 and "
+         "BF_FLAG_MMA_SYNC: mma.sync); key weights tcgen05; decode split-KV (TMA + mma.sync; kept slots: packed fp32)";
 }
 
 }  // extern "C"

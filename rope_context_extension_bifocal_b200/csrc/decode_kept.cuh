@@ -18,8 +18,8 @@
 // cosines, which no table can share since every head has positions of its own). QK^T and PV run on
 // packed fp32 FMAs: with at most 8 query rows they cost less than the conversions and the split
 // operands that the tensor cores would need to keep scores, and so weights, exact to fp32.
-// Measured: 16 sequences of 640 to 8192 slots, 32 / 8 heads of 128 with weights (314 MB): 107 us and 13 us for the
-// merge, 2.8 TB/s of 6.55 with 59% of the issue slots busy; the same rows held in registers instead of a ring in
+// Measured: 16 sequences of 640 to 8192 slots, 32 / 8 heads of 128 with weights (314 MB): 103 us (3.0 TB/s of 6.55, 61%
+// of the issue slots busy) and 14 us for the merge, 112 us the call, where the launches overlap; the same rows held in registers instead of a ring in
 // shared memory (8 warps an SM instead of 16) took 190 us.
 //
 // Work split: a CTA takes a range of slots of one (sequence, kv head), a warp every fourth block of 32 of

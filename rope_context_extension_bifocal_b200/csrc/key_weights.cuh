@@ -29,9 +29,9 @@
 // CTAs share an SM (96 KB and 256 tensor-memory columns each). Many rows (QT = 256): one CTA, two 64 KB query slots,
 // two S tiles of 256 columns, each summed by four groups; wide products, because what the issuing thread does between
 // two visits is idle time of the tensor core (with 128 columns it was half of it).
-// Measured, 32 / 8 heads of 128: last 32 queries of 100003 tokens 191 us (keys alone 32 us at the copy rate; the 11 us
-// a key tile takes are the latency of its steps: load, turn, product, sum), all queries of 6001 tokens 466 us (the
-// three products 273 us at the tensor peak).
+// Measured, 32 / 8 heads of 128: last 32 queries of 100003 tokens 194 us (keys alone 32 us at the copy rate; the 11 us
+// a key tile takes are the latency of its steps: load, turn, product, sum), all queries of 6001 tokens 462 us (the
+// three products 273 us at the tensor peak; tensor pipe 70% busy).
 #pragma once
 #include <type_traits>
 
@@ -292,8 +292,8 @@ __global__ void __launch_bounds__(kw::threads<QT>(), QT == 64 ? 2 : 1) key_weigh
   pdl_launch_dependents();
   pdl_wait();
   const int idx = static_cast<int>(blockIdx.x);
-  // heaviest tiles first over all heads (a head after the other, whose query forms would share L2, took 372 us
-  // instead of 340 at 6001 tokens and as long at 20000, without the product of the queries' low part)
+  // heaviest tiles first over all heads (a head after the other, whose query forms share L2, takes 501 us
+  // instead of 462 at 6001 tokens, 4.01 ms instead of 4.12 at 20000)
   const int kvh = idx % a.hkv, rank = idx / a.hkv;
   const PackedTile tile = a.plan.tiles[rank];
   if (rank >= a.plan.head->n_tiles) return;

@@ -254,9 +254,10 @@ struct KeptLayout {
   int n_split, split_len, pitch;
 };
 
-// Ranges of slots: about 1024 CTAs in all (seven of 128 threads on each SM) as long as a range keeps 64
-// slots, and never more than 512 slots in one, so that a batch of unequal lengths fills the GPU evenly (75.6K slots of
-// 16 sequences: 115 us; ranges of up to 1024 slots 121 us, of 256 118 us, which also costs long caches 18%).
+// Ranges of slots: about 1024 CTAs in all, by the host's bound of the lengths (four of 128 threads are resident on an SM,
+// two with more than four heads a kv head), as long as a range keeps 64 slots, and never more than 512 slots in one, so
+// that a batch of unequal lengths fills the GPU evenly (75.6K slots of
+// 16 sequences: 112 us; ranges of up to 1024 slots 119 us, of 256 112.5 us, which costs two caches of 104K slots in all 5%).
 KeptLayout kept_layout(int batch, int max_len, bool accumulate, const bf_params_t* p) {
   KeptLayout w{};
   const int64_t segs = static_cast<int64_t>(batch) * p->hkv;
@@ -342,7 +343,7 @@ bf_status_t decode_kept_impl(const void* q, const void* k_new, const void* v_new
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const Rope rope = make_rope(p->rope_theta, p->head_dim, 1);
   // A stage's slots share a page, and are one box of the pool, where pages hold whole stages; other page sizes are
-  // copied row by row (75.6K slots: 114 us with pages of 64, 135 us with pages of 12).
+  // copied row by row (75.6K slots: 112 us with pages of 64, 133 us with pages of 12).
   a.boxes = page_size % (bf::kept::STAGE_BYTES / (4 * p->head_dim)) == 0 ? 1 : 0;
   if (a.boxes && (!make_slot_map(&a.k_map, kcache, cache_rows, p->hkv, p->head_dim) ||
                   !make_slot_map(&a.v_map, vcache, cache_rows, p->hkv, p->head_dim)))
@@ -551,8 +552,8 @@ bf_status_t key_weights_impl(const void* q, const void* k, int32_t dtype, const 
   const int g = p->hq / p->hkv;
   if (lay.max_tiles * p->hkv > 0x7fffffffLL || lay.rows * g > 0x7ffffe00LL || p->hq > 65535)
     return BF_ERR_UNSUPPORTED;
-  // Few rows a key tile: 64-row query tiles, two CTAs an SM. Of 27461 tokens, 4 heads a kv head: 256 rows 87 us (with
-  // 256-row tiles 113), 512 rows 128 us (138), 1024 rows 214 us with 64-row tiles and 202 with 256-row ones.
+  // Few rows a key tile: 64-row query tiles, two CTAs an SM. Of 27461 tokens, 4 heads a kv head: 256 rows 89 us (with
+  // 256-row tiles 108), 512 rows 129 us (132), 1024 rows 215 us with 64-row tiles and 199 with 256-row ones.
   const int qt = static_cast<int64_t>(obs) * g <= 512 ? 64 : 256;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
